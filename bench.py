@@ -213,7 +213,8 @@ def parse():
     return ap.parse_args()
 
 
-def kernel_source_hash(files=("kd_kernels.hip", "kd_api.hip", "kd_internal.h")):
+def kernel_source_hash(files=("kd_gemm.h", "kd_kernels.hip", "kd_api.hip",
+                              "kd_internal.h")):
     """Hash of the sources that the counters were taken on, comments and whitespace
     removed: a change of the code (not of its comments) makes the record stale."""
     import re

@@ -58,7 +58,8 @@ std::mutex g_prof_mu;
 
 const char *const kClassNames[kd::KC_COUNT] = {
     "validate", "fwd_gemm_lse", "bucket", "combine_lse_loss", "bwd_gemm_dz",
-    "scatter",  "dh_gemm",      "dh_reduce", "dw_gemm",      "transpose", "teacher_topk", "dz_rescale", "misc"};
+    "scatter",  "dh_gemm",      "dh_reduce", "dw_gemm",      "transpose", "teacher_topk", "dz_rescale", "misc",
+    "token_logprobs", "token_logprobs_bwd", "clip_grads"};
 
 #define HIPCHK(expr)                                                                 \
   do {                                                                               \
@@ -101,6 +102,18 @@ int check_sizes(int64_t N, int64_t d, int64_t V, int32_t K, int64_t chunk, int32
 }  // namespace
 
 namespace kd {
+
+int set_error(int code, const char *fmt, ...) {
+  if (!fmt) {
+    g_err[0] = 0;
+    return code;
+  }
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
 
 void prof_begin(int cls, hipStream_t s) {
   if (!g_prof.on) return;

@@ -37,6 +37,9 @@ enum KClass {
   KC_TOPK,         // teacher top-K cache producer
   KC_RESCALE,      // single-sweep backward: exp(z - max) rescaled into dz
   KC_MISC,         // fills, loss accumulation and finalisation
+  KC_LOGPROBS,     // log probabilities of given tokens (rows of logits, partials, joins)
+  KC_LOGPROBS_BWD, // their gradient
+  KC_CLIP,         // gradient norm and clipping
   KC_COUNT
 };
 
@@ -170,7 +173,9 @@ hipError_t topk_scratch(int **out);
 hipError_t launch_teacher_topk(int dtype, const void *logits, int64_t N, int64_t V, int32_t K,
                                int32_t *idx, float *p, float *lse, int *flags, hipStream_t s);
 
-// --- timing hooks (kd_api.hip) ---
+// --- errors and timing hooks (kd_api.hip) ---
+// Sets (fmt) or clears (fmt null) the text kd_last_error() gives on this thread; returns code.
+int set_error(int code, const char *fmt, ...);
 void prof_begin(int cls, hipStream_t s);
 void prof_end(int cls, hipStream_t s);
 
