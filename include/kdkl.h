@@ -357,10 +357,66 @@ int kd_teacher_topk_noalloc(const void *logits, int32_t dtype, int64_t N, int64_
                             int32_t K, int32_t *topk_idx, float *topk_p, float *row_lse,
                             void *stream);
 
+/*
+ * Log probabilities of given tokens, from logits.
+ *
+ * For row n of logits z[n, 0..V) with the given token t = tokens[n]:
+ *   row_lse[n] = log sum_v exp z[n,v]
+ *   logp[n]    = z[n,t] - row_lse[n]                 (0 where t < 0: the row has no token)
+ *   entropy[n] = - sum_v p log p,  p = exp(z[n,v] - row_lse[n])       (0 log 0 = 0)
+ *   top_idx[n,k], top_logp[n,k], k < top: the tokens with the largest logits and their log
+ *                p, in decreasing order of logit; equal logits in increasing token order
+ *                (+0.0 == -0.0)
+ * Logits of -inf (masked tokens) have probability 0; a row with no finite logit has
+ * row_lse = logp = top_logp = -inf (logp 0 without a token), entropy 0 and the first `top`
+ * tokens.  A row with a NaN or +inf logit gets NaN in every result and -1 in top_idx; a
+ * token t >= V gives logp NaN.  Both set status[0] = KD_E_INDEX if status is given.
+ *
+ *   logits    [N] rows of V elements of dtype (KD_BF16 or KD_F32), ld elements apart
+ *             (ld >= V when N > 1), aligned to the element
+ *   tokens    [N]  int32 (token_bits 32) or int64 (token_bits 64)
+ *   logp, entropy, row_lse [N] float32 (required)
+ *   row_stats [N, 2] float32 (max, log sum exp(z - max)): the state
+ *             kd_token_logprobs_bwd reads; 8-byte aligned; NULL = skip
+ *   top_idx [N, top] int32, top_logp [N, top] float32: required when top > 0
+ *   status    [1] int32 or NULL; set in the cases above and never cleared by the call
+ *   workspace 256-byte aligned, kd_token_logprobs_workspace_bytes(...) bytes (0 for many
+ *             rows: then NULL is allowed).  It keeps nothing between calls; calls that
+ *             may overlap need one each.
+ * Sizes: 0 <= N < 2^24, 1 <= V < 2^29, 0 <= top <= min(V, 64).  Sums are float32 over a few
+ * elements and float64 beyond; results do not depend on timing.  Nothing is synchronised,
+ * copied or allocated: every device operation is a kernel launch on `stream`, so the call
+ * can be recorded into a HIP graph.  Errors: host-side checks before any device work.
+ */
+int kd_token_logprobs_workspace_bytes(int64_t N, int64_t V, int32_t top, int32_t dtype,
+                                      size_t *bytes_out);
+int kd_token_logprobs(const void *logits, int32_t dtype, int64_t ld, const void *tokens,
+                      int32_t token_bits, int64_t N, int64_t V, int32_t top, float *logp,
+                      float *entropy, float *row_lse, float *row_stats, int32_t *top_idx,
+                      float *top_logp, int32_t *status, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * kd_token_logprobs_bwd -- the gradient of the logits, for upstream gradients gl of logp, ge
+ * of entropy and gz of row_lse (each [N] float32; NULL = 0):
+ *   dlogits[n,v] = p (gz - gl - ge (log p + entropy[n])) + gl [v = t]
+ * with gl taken as 0 where t < 0.  A row with no finite logit gets 0, a row that was
+ * invalid in the forward call (or whose token is >= V) NaN.
+ *   row_stats, entropy  from kd_token_logprobs on the same logits
+ *   dlogits [N] rows of V elements of dtype, ld_d elements apart; rounded once (RNE); may be
+ *           logits itself (same address and, when N > 1, ld_d == ld), may not overlap it
+ *           otherwise.  Elements between V and ld_d are left as they were.
+ * Limits, stream behaviour and errors as kd_token_logprobs; no workspace.
+ */
+int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const void *tokens,
+                          int32_t token_bits, int64_t N, int64_t V, const float *row_stats,
+                          const float *entropy, const float *grad_logp, const float *grad_entropy,
+                          const float *grad_lse, void *dlogits, int64_t ld_d, void *stream);
+
 /* Text describing the last non-OK return on the calling thread ("" if none). */
 const char *kd_last_error(void);
 
-/* Library interface version: 5 (it increments when a call is added or changes). */
+/* Interface version of the loss calls: 5 (it increments when one of them is added or changes). */
 int kd_version(void);
 
 /*

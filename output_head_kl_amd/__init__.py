@@ -14,7 +14,8 @@ from typing import Optional
 
 __all__ = ["KDError", "library_path", "workspace_bytes", "fwd_bwd", "fwd", "bwd",
            "chunked_kl_loss", "scale_grads", "teacher_topk", "vocab_shard_fwd", "vocab_shard_combine",
-           "vocab_shard_bwd", "profile_enable", "profile_read", "profile_classes", "KD_F32",
+           "vocab_shard_bwd", "token_logprobs", "token_logprobs_bwd",
+           "token_logprobs_workspace_bytes", "profile_enable", "profile_read", "profile_classes", "KD_F32",
            "KD_BF16"]
 
 KD_F32, KD_BF16 = 0, 1
@@ -96,6 +97,8 @@ def _lib():
     lib.kd_clock_stamp.restype = ctypes.c_int
     lib.kd_wall_clock_khz.argtypes = [ctypes.POINTER(i32)]
     lib.kd_wall_clock_khz.restype = ctypes.c_int
+    from . import _ops
+    _ops.declare(lib)
     _LIB = lib
     return lib
 
@@ -548,3 +551,12 @@ def profile_read():
         _check(lib.kd_profile_read(i, ctypes.byref(ms), ctypes.byref(n)))
         out[name] = (ms.value, n.value)
     return out
+
+
+def __getattr__(name):
+    # the operators beside the loss need torch at import; the module loads with first use
+    if name in __all__:
+        from . import _ops
+        globals()[name] = getattr(_ops, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

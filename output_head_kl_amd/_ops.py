@@ -1,0 +1,199 @@
+"""The operators beside the loss: log probabilities of given tokens (from logits) with their
+gradient.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
+allocated with torch, and the library's HIP kernels do the work on the current stream (or on
+``stream``).  No call synchronises, so each can be recorded with ``torch.cuda.graph``."""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+import output_head_kl_amd as kd
+
+_F32 = torch.float32
+
+
+def declare(lib) -> None:
+    """Argument types of the operators' C calls."""
+    i64, i32, vp, sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+    psz = ctypes.POINTER(sz)
+    for name, args in (
+            ("kd_token_logprobs_workspace_bytes", [i64, i64, i32, i32, psz]),
+            ("kd_token_logprobs", [vp, i32, i64, vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp,
+                                   vp, vp, sz, vp]),
+            ("kd_token_logprobs_bwd", [vp, i32, i64, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp,
+                                       i64, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The call's device and stream as torch's current ones, so that what the call allocates
+    belongs to the stream that uses it."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _elsewhere(dev, stream) -> bool:
+    """Whether the call needs ``_on``: another stream or another device than the current."""
+    return stream is not None or torch.cuda.current_device() != dev.index
+
+
+def _rows(t, name):
+    """(N, V, elements between rows) of a 2-D tensor whose rows are contiguous and apart."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, not {t.dim()}-D")
+    N, V = t.shape
+    if V < 1 or (V > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < V):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap "
+                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
+    return N, V, t.stride(0) if N > 1 else V
+
+
+def _token_bits(tokens, N):
+    if tokens.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens must be int32 or int64, not {tokens.dtype}")
+    if tokens.dim() != 1 or tokens.shape[0] != N or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous tensor of shape [{N}]")
+    return 64 if tokens.dtype == torch.int64 else 32
+
+
+def _status_ptr(status):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise ValueError("status must be a one-element int32 tensor")
+    return status.data_ptr()
+
+
+def _upstream(name, g, N, dev):
+    """An upstream gradient as the library reads it: None, or contiguous float32 [N]."""
+    if g is None:
+        return None
+    kd._on_device(dev, **{name: g})
+    if tuple(g.shape) != (N,):
+        raise ValueError(f"{name} must have shape [{N}]")
+    return g.to(_F32).contiguous()
+
+
+def _float_rows(name, t, shape):
+    if t.dtype != _F32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    kd._check_workspace(workspace, dev)
+    return workspace
+
+
+def token_logprobs_workspace_bytes(N: int, V: int, top: int = 0, dtype: int = kd.KD_BF16) -> int:
+    """Workspace bytes of ``token_logprobs`` (0 for many rows)."""
+    out = ctypes.c_size_t(0)
+    kd._check(kd._lib().kd_token_logprobs_workspace_bytes(N, V, top, dtype, ctypes.byref(out)))
+    return int(out.value)
+
+
+def _token_logprobs(logits, tokens, top, status, workspace, stats):
+    dt = kd._dtype_code(logits)
+    dev = logits.device
+    kd._on_device(dev, logits=logits, tokens=tokens, status=status)
+    N, V, ld = _rows(logits, "logits")
+    bits = _token_bits(tokens, N)
+    workspace = _scratch(workspace, token_logprobs_workspace_bytes(N, V, top, dt), dev)
+    logp = torch.empty(N, dtype=_F32, device=dev)
+    entropy = torch.empty(N, dtype=_F32, device=dev)
+    lse = torch.empty(N, dtype=_F32, device=dev)
+    st = torch.empty((N, 2), dtype=_F32, device=dev) if stats else None
+    idx = torch.empty((N, top), dtype=torch.int32, device=dev) if top else None
+    tlp = torch.empty((N, top), dtype=_F32, device=dev) if top else None
+    kd._check(kd._lib().kd_token_logprobs(
+        logits.data_ptr(), dt, ld, tokens.data_ptr(), bits, N, V, top, logp.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), kd._ptr(st), kd._ptr(idx), kd._ptr(tlp),
+        _status_ptr(status), kd._ptr(workspace), 0 if workspace is None else workspace.numel(),
+        torch.cuda.current_stream(dev).cuda_stream))
+    return (logp, entropy, lse, idx, tlp) if top else (logp, entropy, lse), st
+
+
+def token_logprobs(logits, tokens, top: int = 0, status=None, workspace=None, stream=None):
+    """Log probabilities of given tokens from logits, with entropy and top alternatives.
+
+    Args (torch CUDA tensors):
+      logits [N, V]: bfloat16 or float32, rows contiguous (any distance between rows);
+      tokens [N]: int32 or int64, negative where a row has no token.
+      top: number of alternatives, 0 to 64.
+      status: optional int32 tensor of one element, set to 2 (KD_E_INDEX) when a token is
+        not below V or a row holds NaN or +inf (never cleared).
+      workspace: optional uint8 tensor of ``token_logprobs_workspace_bytes`` bytes.
+      stream: a torch.cuda.Stream or a raw handle; the current stream by default.
+    Returns (logp [N], entropy [N], lse [N]) float32 and, with ``top``, (top_idx [N, top]
+    int32, top_logp [N, top] float32), the largest logits first, equal ones by rising index.
+    logp is 0 without a token; a row with no finite logit has logp = lse = -inf, entropy 0; an
+    invalid row NaN.  logp, entropy and lse are differentiable in logits (the alternatives are
+    not); the backward reads logits again."""
+    dev = logits.device
+    kd._on_device(dev, logits=logits)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return token_logprobs(logits, tokens, top, status, workspace)
+    if torch.is_grad_enabled() and logits.requires_grad:
+        return _TokenLogprobs.apply(logits, tokens, top, status, workspace)
+    return _token_logprobs(logits, tokens, top, status, workspace, False)[0]
+
+
+def token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp=None, grad_entropy=None,
+                       grad_lse=None, out=None, stream=None):
+    """The gradient of the logits (kd_token_logprobs_bwd) for upstream gradients [N] of logp,
+    entropy and lse (None: 0).  ``row_stats`` [N, 2] and ``entropy`` [N] come from the
+    forward; ``out`` may be given, and may be ``logits`` itself."""
+    dev = logits.device
+    kd._on_device(dev, logits=logits, tokens=tokens, row_stats=row_stats, entropy=entropy, out=out)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp,
+                                      grad_entropy, grad_lse, out)
+    dt = kd._dtype_code(logits)
+    N, V, ld = _rows(logits, "logits")
+    bits = _token_bits(tokens, N)
+    _float_rows("row_stats", row_stats, (N, 2))
+    _float_rows("entropy", entropy, (N,))
+    g = [_upstream(n, x, N, dev) for n, x in (("grad_logp", grad_logp),
+                                              ("grad_entropy", grad_entropy),
+                                              ("grad_lse", grad_lse))]
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    if out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must have the shape and dtype of logits")
+    ld_d = _rows(out, "out")[2]
+    kd._check(kd._lib().kd_token_logprobs_bwd(
+        logits.data_ptr(), dt, ld, tokens.data_ptr(), bits, N, V, row_stats.data_ptr(),
+        entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]), out.data_ptr(), ld_d,
+        torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top, status, workspace):
+        ctx.set_materialize_grads(False)
+        outs, st = _token_logprobs(logits, tokens, top, status, workspace, True)
+        ctx.save_for_backward(logits, tokens, st, outs[1])
+        if top:
+            ctx.mark_non_differentiable(*outs[3:])
+        return outs
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logp, g_entropy, g_lse, *_):
+        logits, tokens, st, entropy = ctx.saved_tensors
+        grad = token_logprobs_bwd(logits, tokens, st, entropy, g_logp, g_entropy, g_lse)
+        return grad, None, None, None, None

@@ -1,0 +1,84 @@
+// Internal interface of the operators beside the loss: log probabilities of given tokens
+// (from logits and from hidden states) with their gradients, and gradient clipping.
+#pragma once
+
+#include "kd_internal.h"
+
+namespace kd {
+
+// ln(x) and 2^x of the hardware work in base 2.
+constexpr float kOpLog2e = 1.4426950408889634f;
+constexpr double kOpLn2d = 0.6931471805599453;
+// Lower bound put on ln p where it multiplies p: p is 0 below about -104, and 0 * -inf is NaN.
+constexpr float kOpLowest = -1.0e4f;
+
+// The given tokens: int32 or int64, negative = the row has none.
+struct Tokens {
+  const void *ptr;
+  int wide;  // 1: int64
+  __device__ __forceinline__ long long at(long long n) const {
+    return wide ? ((const long long *)ptr)[n] : (long long)((const int *)ptr)[n];
+  }
+};
+
+// Per-row results.  stats[n] = (max, ln sum exp(z - max)), the state the gradients read
+// (kept apart: their sum would lose digits of ln p where the maximum is large).
+struct LpOut {
+  float *logp, *entropy, *lse;
+  float2 *stats;       // may be null
+  int32_t *top_idx;    // [N][top], null when top == 0
+  float *top_logp;
+  int32_t *status;     // may be null; set to bad_code, never cleared
+  int bad_code;
+};
+
+// Writes a row's results from its maximum m, S = sum exp(z - m), T = sum exp(z - m)(z - m)
+// and the given token's logit zt.  No finite logit (S = 0): lse = logp = -inf, entropy 0.
+// A NaN or +inf logit (S is NaN): everything NaN.  Returns ln S (double), NaN for a bad row
+// and -inf for an empty one.
+__device__ __forceinline__ double lp_finish(const LpOut &o, long long n, float m, double S,
+                                            double T, long long tok, long long V, float zt) {
+  const float nan = __uint_as_float(0x7FC00000u);
+  const bool bad = !(S >= 0.0) || !(m < INFINITY), empty = !bad && S == 0.0;
+  double lnS = empty ? -(double)INFINITY : log(S);
+  float lp, H, lse, mm = m;
+  if (bad) {
+    lp = H = lse = mm = nan;
+    lnS = (double)nan;
+  } else if (empty) {
+    lp = lse = mm = -INFINITY;
+    H = 0.f;
+  } else {
+    lp = (float)((double)zt - (double)m - lnS);
+    const double h = lnS - T / S;
+    H = h > 0.0 ? (float)h : 0.f;
+    lse = (float)((double)m + lnS);
+  }
+  if (tok < 0) lp = bad ? nan : 0.f;
+  if (tok >= V) lp = nan;
+  o.logp[n] = lp;
+  o.entropy[n] = H;
+  o.lse[n] = lse;
+  if (o.stats) o.stats[n] = make_float2(mm, empty ? 0.f : (float)lnS);
+  if (o.status && (bad || tok >= V)) *o.status = o.bad_code;
+  return lnS;
+}
+
+// --- log probabilities from logits (kd_logprobs.hip) ---
+constexpr int kLpMaxTop = 64;  // one alternative per lane of a wave
+// Vocabulary splits of a row (1: no workspace and one launch).
+int lp_splits(int64_t N, int64_t V, int dtype);
+size_t lp_workspace(int64_t N, int64_t V, int32_t top, int dtype);
+hipError_t launch_token_logprobs(int dtype, const void *logits, int64_t ld, const Tokens &tokens,
+                                 int64_t N, int64_t V, int32_t top, const LpOut &out, void *ws,
+                                 hipStream_t s);
+// Upstream gradients may be null (zero).  dlogits may be logits itself when ld_d == ld.
+struct LpGrad {
+  const float2 *stats;
+  const float *entropy, *g_logp, *g_entropy, *g_lse;
+};
+hipError_t launch_token_logprobs_bwd(int dtype, const void *logits, int64_t ld,
+                                     const Tokens &tokens, int64_t N, int64_t V, const LpGrad &g,
+                                     void *dlogits, int64_t ld_d, hipStream_t s);
+
+}  // namespace kd
