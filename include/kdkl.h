@@ -413,6 +413,28 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
                           const float *entropy, const float *grad_logp, const float *grad_entropy,
                           const float *grad_lse, void *dlogits, int64_t ld_d, void *stream);
 
+/*
+ * kd_clip_grads -- the global norm of gradients (dh, dW and whatever else a step trains) and
+ * clipping to max_norm.
+ *   norm[0]  = sqrt(sum over all n tensors of the sum of g^2)     (squares summed in float64)
+ *   out      = g * (max_norm / norm) rounded once to the tensor's type (RNE) where the norm
+ *              exceeds max_norm and is finite in float32, else g as it is
+ *   grads, outs  host arrays of n device addresses; outs == NULL: in place.  An address of
+ *                an empty tensor may be NULL; the others aligned to their element
+ *   numel, dtypes host arrays of n element counts and types (KD_F32, KD_BF16; mixed is fine)
+ *   max_norm     >= 0; infinity with outs == NULL computes the norm only
+ *   norm [1] float32 device;  workspace 256-byte aligned, kd_clip_grads_workspace_bytes bytes,
+ *                one for each call that may overlap another
+ * The host arrays are read before the call returns.  Tensors to be written may not share
+ * memory with each other or with another tensor's gradient (KD_E_ARG); outs[i] == grads[i]
+ * is fine.  Results do not depend on timing.  No synchronisation, copy or allocation on the
+ * device: the call can be recorded into a HIP graph.  At most 2^44 elements in all.
+ */
+int kd_clip_grads_workspace_bytes(const int64_t *numel, int32_t n, size_t *bytes_out);
+int kd_clip_grads(const void *const *grads, void *const *outs, const int64_t *numel,
+                  const int32_t *dtypes, int32_t n, float max_norm, float *norm, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
 /* Text describing the last non-OK return on the calling thread ("" if none). */
 const char *kd_last_error(void);
 

@@ -1,5 +1,5 @@
 """The operators beside the loss: log probabilities of given tokens (from logits) with their
-gradient.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
+gradient, and the gradient norm with clipping.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
 allocated with torch, and the library's HIP kernels do the work on the current stream (or on
 ``stream``).  No call synchronises, so each can be recorded with ``torch.cuda.graph``."""
 from __future__ import annotations
@@ -23,7 +23,9 @@ def declare(lib) -> None:
             ("kd_token_logprobs", [vp, i32, i64, vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp,
                                    vp, vp, sz, vp]),
             ("kd_token_logprobs_bwd", [vp, i32, i64, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp,
-                                       i64, vp])):
+                                       i64, vp]),
+            ("kd_clip_grads_workspace_bytes", [vp, i32, psz]),
+            ("kd_clip_grads", [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
 
@@ -197,3 +199,66 @@ class _TokenLogprobs(torch.autograd.Function):
         logits, tokens, st, entropy = ctx.saved_tensors
         grad = token_logprobs_bwd(logits, tokens, st, entropy, g_logp, g_entropy, g_lse)
         return grad, None, None, None, None
+
+
+def _clip(grads, max_norm, out, workspace, stream):
+    if not grads:
+        raise ValueError("no tensors")
+    dev = grads[0].device
+    kd._on_device(dev, grads=grads[0])
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _clip(grads, max_norm, out, workspace, None)
+    n = len(grads)
+    if out is not None and len(out) != n:
+        raise ValueError(f"{len(out)} outputs for {n} gradients")
+    codes = {torch.bfloat16: kd.KD_BF16, _F32: kd.KD_F32}
+    for name, ts in (("grads", grads), ("out", out or ())):
+        for i, t in enumerate(ts):
+            if t.device != dev:
+                kd._on_device(dev, **{f"{name}[{i}]": t})
+            if t.dtype not in codes:
+                raise TypeError(f"{name}[{i}] must be bfloat16 or float32, not {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+            if name == "out" and (t.dtype != grads[i].dtype or t.shape != grads[i].shape):
+                raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
+    numel = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    types = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in grads])
+    gp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    op = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        kd._check(kd._lib().kd_clip_grads_workspace_bytes(numel, n, ctypes.byref(need)))
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    else:
+        kd._check_workspace(workspace, dev)
+    norm = torch.empty(1, dtype=_F32, device=dev)
+    kd._check(kd._lib().kd_clip_grads(gp, op, numel, types, n, max_norm, norm.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(),
+                                      torch.cuda.current_stream(dev).cuda_stream))
+    return norm
+
+
+def grad_norm(grads, workspace=None, stream=None):
+    """The global norm [1] (float32) of a list of contiguous bfloat16 or float32 CUDA tensors,
+    mixed as they come: sqrt of the sum of all squares, summed in float64."""
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    return _clip(grads, float("inf"), None, workspace, stream)
+
+
+@torch.no_grad()
+def clip_grads(grads, max_norm: float, out=None, workspace=None, stream=None):
+    """Clips gradients to a global norm (kd_clip_grads): returns the norm [1] (float32) before
+    clipping; where it exceeds ``max_norm`` (and is finite) every tensor is scaled by
+    max_norm / norm, in place or into ``out``, tensors of the same shapes and types (which
+    get the gradients as they are otherwise).  ``grads`` as in ``grad_norm``; a tensor may
+    not appear twice."""
+    grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+    norm = _clip(grads, float(max_norm), out, workspace, stream)
+    # written behind autograd's back: a backward that saved one of these must notice
+    torch.autograd.graph.increment_version(
+        [t for t in (grads if out is None else out) if not t.is_inference()])
+    return norm

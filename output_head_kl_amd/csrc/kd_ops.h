@@ -81,4 +81,12 @@ hipError_t launch_token_logprobs_bwd(int dtype, const void *logits, int64_t ld,
                                      const Tokens &tokens, int64_t N, int64_t V, const LpGrad &g,
                                      void *dlogits, int64_t ld_d, hipStream_t s);
 
+// --- gradient norm and clipping (kd_clip.hip) ---
+// Float64 partials of the squares' sum (one per chunk of a tensor).
+int64_t clip_partials(const int64_t *numel, int32_t n);
+// scale false: the norm only.  outs null: in place.  Host arrays, read before the return.
+hipError_t launch_clip_grads(const void *const *grads, void *const *outs, const int64_t *numel,
+                             const int32_t *dtypes, int32_t n, bool scale, float max_norm,
+                             float *norm, double *part, hipStream_t s);
+
 }  // namespace kd

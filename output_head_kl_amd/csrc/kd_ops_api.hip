@@ -4,6 +4,10 @@
 #include "kd_ops.h"
 #include "kdkl.h"
 
+#include <algorithm>
+#include <new>
+#include <vector>
+
 namespace {
 
 using kd::set_error;
@@ -33,6 +37,51 @@ int check_logits(const void *logits, int32_t dtype, int64_t ld, const void *toke
   if (N > 0 && (!logits || !tokens)) return set_error(KD_E_ARG, "logits and tokens are required when N > 0");
   if (mis(logits, dtype == KD_BF16 ? 2 : 4)) return set_error(KD_E_ARG, "logits misaligned");
   if (mis(tokens, token_bits / 8)) return set_error(KD_E_ARG, "tokens misaligned");
+  return KD_OK;
+}
+
+int check_tensors(const int64_t *numel, int32_t n) {
+  if (n < 0) return set_error(KD_E_ARG, "n = %d < 0", n);
+  if (n > 0 && !numel) return set_error(KD_E_ARG, "numel is required when n > 0");
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] < 0) return set_error(KD_E_ARG, "numel[%d] = %lld < 0", i, (long long)numel[i]);
+    if (numel[i] > ((int64_t)1 << 44) || (total += numel[i]) > ((int64_t)1 << 44))
+      return set_error(KD_E_UNSUPPORTED, "more than 2^44 elements");
+  }
+  return KD_OK;
+}
+
+struct Span {
+  uintptr_t lo, hi;
+  int32_t i;
+};
+
+// Every element is written once, and only its own tensor's gradient may share its place.
+int check_overlap(const void *const *grads, void *const *outs, const int64_t *numel,
+                  const int32_t *dtypes, int32_t n) {
+  std::vector<Span> w;
+  w.reserve((size_t)n);
+  auto bytes = [&](int32_t i) { return (uintptr_t)numel[i] * (dtypes[i] == KD_BF16 ? 2 : 4); };
+  for (int32_t i = 0; i < n; ++i)
+    if (numel[i] > 0) {
+      const uintptr_t p = (uintptr_t)(outs ? outs[i] : grads[i]);
+      w.push_back({p, p + bytes(i), i});
+    }
+  std::sort(w.begin(), w.end(), [](const Span &a, const Span &b) { return a.lo < b.lo; });
+  for (size_t k = 1; k < w.size(); ++k)
+    if (w[k].lo < w[k - 1].hi)
+      return set_error(KD_E_ARG, "tensors %d and %d to be written share memory", w[k - 1].i, w[k].i);
+  if (!outs) return KD_OK;
+  for (int32_t i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t lo = (uintptr_t)grads[i], hi = lo + bytes(i);
+    auto it = std::upper_bound(w.begin(), w.end(), lo,
+                               [](uintptr_t x, const Span &s) { return x < s.hi; });
+    for (; it != w.end() && it->lo < hi; ++it)
+      if (!(it->i == i && it->lo == lo))
+        return set_error(KD_E_ARG, "output %d shares memory with gradient %d", it->i, i);
+  }
   return KD_OK;
 }
 
@@ -119,6 +168,53 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
   LAUNCH(kd::KC_LOGPROBS_BWD,
          kd::launch_token_logprobs_bwd(dtype, logits, ld, kd::Tokens{tokens, token_bits == 64}, N,
                                        V, g, dlogits, ld_d, stream));
+  return KD_OK;
+}
+
+int kd_clip_grads_workspace_bytes(const int64_t *numel, int32_t n, size_t *bytes_out) {
+  set_error(KD_OK, nullptr);
+  if (!bytes_out) return set_error(KD_E_ARG, "bytes_out is NULL");
+  int rc = check_tensors(numel, n);
+  if (rc != KD_OK) return rc;
+  *bytes_out = (size_t)rup((kd::clip_partials(numel, n) + 1) * 8, 256);
+  return KD_OK;
+}
+
+int kd_clip_grads(const void *const *grads, void *const *outs, const int64_t *numel,
+                  const int32_t *dtypes, int32_t n, float max_norm, float *norm, void *workspace,
+                  size_t workspace_bytes, void *stream_v) {
+  set_error(KD_OK, nullptr);
+  int rc = check_tensors(numel, n);
+  if (rc != KD_OK) return rc;
+  if (!(max_norm >= 0.f)) return set_error(KD_E_ARG, "max_norm must be >= 0 (infinity: no clipping)");
+  if (n > 0 && (!grads || !dtypes)) return set_error(KD_E_ARG, "grads and dtypes are required when n > 0");
+  if (!norm || mis(norm, 4)) return set_error(KD_E_ARG, "norm is required, 4-byte aligned");
+  for (int32_t i = 0; i < n; ++i) {
+    if (dtypes[i] != KD_F32 && dtypes[i] != KD_BF16)
+      return set_error(KD_E_ARG, "dtypes[%d] = %d unknown", i, dtypes[i]);
+    if (numel[i] == 0) continue;
+    const uintptr_t es = dtypes[i] == KD_BF16 ? 2 : 4;
+    if (!grads[i] || (outs && !outs[i])) return set_error(KD_E_ARG, "tensor %d is NULL", i);
+    if (mis(grads[i], es) || (outs && mis(outs[i], es)))
+      return set_error(KD_E_ARG, "tensor %d is misaligned", i);
+  }
+  const bool scale = outs || max_norm < __builtin_huge_valf();
+  if (scale) {
+    try {
+      rc = check_overlap(grads, outs, numel, dtypes, n);
+    } catch (const std::bad_alloc &) {
+      return set_error(KD_E_ARG, "out of host memory for %d tensors", n);
+    }
+    if (rc != KD_OK) return rc;
+  }
+  const size_t need = (size_t)rup((kd::clip_partials(numel, n) + 1) * 8, 256);
+  if (!workspace) return set_error(KD_E_WORKSPACE, "workspace is required (%zu bytes)", need);
+  if (mis(workspace, 256)) return set_error(KD_E_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return set_error(KD_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  hipStream_t stream = (hipStream_t)stream_v;
+  LAUNCH(kd::KC_CLIP, kd::launch_clip_grads(grads, outs, numel, dtypes, n, scale, max_norm, norm,
+                                            (double *)workspace, stream));
   return KD_OK;
 }
 
