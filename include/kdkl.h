@@ -414,6 +414,45 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
                           const float *grad_lse, void *dlogits, int64_t ld_d, void *stream);
 
 /*
+ * Log probabilities of given tokens, from hidden states: kd_token_logprobs's logp, entropy
+ * and row_lse for z = h W^T, with no logits in memory (one chunk of tokens at a time, only
+ * its per-tile partial sums are kept), and the gradients with z recomputed.
+ *
+ * kd_head_logprobs
+ *   h [N, d], W [V, d] dtype, row-major, contiguous, 16-byte aligned
+ *   tokens, logp, entropy, row_lse, row_stats, status  as kd_token_logprobs
+ *   workspace  256-byte aligned, kd_head_logprobs_workspace_bytes(...) bytes
+ * Products are exact and summed in float32.  A row whose logits are not all finite gets NaN.
+ *
+ * kd_head_logprobs_bwd: for upstream gradients gl, ge, gz of logp, entropy and row_lse
+ *   ([N] float32; NULL = 0), with dz as in kd_token_logprobs_bwd (rounded to dtype once):
+ *   dh = dz W  [N, d] dtype, rounded once;  dW = dz^T h  [V, d] float32, overwritten
+ *   (each 16-byte aligned; either may be NULL: not wanted)
+ *   row_stats, entropy  from kd_head_logprobs on the same h and W
+ *   workspace  kd_head_logprobs_bwd_workspace_bytes(..., 16384, ...) bytes for full speed, at
+ *              least (..., 0, ...) bytes; dw_group_tokens as kd_workspace_bytes_group
+ * A token >= V makes its row of dh and all of dW NaN.
+ *
+ * Sizes: N >= 0, d >= 8 with d % 8 == 0, d <= 2^20, 1 <= V <= 2^24, chunk >= 1, min(chunk, N)
+ * <= 2^22.  Results do not depend on timing, and on chunk (of the forward) not at all.  No
+ * synchronisation, copy or allocation: every call can be recorded into a HIP graph.
+ */
+int kd_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
+                                     int32_t dtype, size_t *bytes_out);
+int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *tokens,
+                     int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                     float *logp, float *entropy, float *row_lse, float *row_stats,
+                     int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+int kd_head_logprobs_bwd_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
+                                         int32_t dtype, int64_t dw_group_tokens,
+                                         size_t *bytes_out);
+int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void *tokens,
+                         int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                         const float *row_stats, const float *entropy, const float *grad_logp,
+                         const float *grad_entropy, const float *grad_lse, void *dh, float *dW,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * kd_clip_grads -- the global norm of gradients (dh, dW and whatever else a step trains) and
  * clipping to max_norm.
  *   norm[0]  = sqrt(sum over all n tensors of the sum of g^2)     (squares summed in float64)

@@ -15,7 +15,9 @@ from typing import Optional
 __all__ = ["KDError", "library_path", "workspace_bytes", "fwd_bwd", "fwd", "bwd",
            "chunked_kl_loss", "scale_grads", "teacher_topk", "vocab_shard_fwd", "vocab_shard_combine",
            "vocab_shard_bwd", "token_logprobs", "token_logprobs_bwd",
-           "token_logprobs_workspace_bytes", "grad_norm", "clip_grads", "profile_enable", "profile_read", "profile_classes", "KD_F32",
+           "token_logprobs_workspace_bytes", "head_logprobs", "head_logprobs_bwd",
+           "head_logprobs_workspace_bytes", "head_logprobs_bwd_workspace_bytes", "grad_norm",
+           "clip_grads", "profile_enable", "profile_read", "profile_classes", "KD_F32",
            "KD_BF16"]
 
 KD_F32, KD_BF16 = 0, 1

@@ -1,5 +1,5 @@
-"""The operators beside the loss: log probabilities of given tokens (from logits) with their
-gradient, and the gradient norm with clipping.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
+"""The operators beside the loss: log probabilities of given tokens (from logits
+and from hidden states) with their gradients, and the gradient norm with clipping.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
 allocated with torch, and the library's HIP kernels do the work on the current stream (or on
 ``stream``).  No call synchronises, so each can be recorded with ``torch.cuda.graph``."""
 from __future__ import annotations
@@ -24,6 +24,12 @@ def declare(lib) -> None:
                                    vp, vp, sz, vp]),
             ("kd_token_logprobs_bwd", [vp, i32, i64, vp, i32, i64, i64, vp, vp, vp, vp, vp, vp,
                                        i64, vp]),
+            ("kd_head_logprobs_workspace_bytes", [i64, i64, i64, i64, i32, psz]),
+            ("kd_head_logprobs", [vp, vp, i32, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                  vp, sz, vp]),
+            ("kd_head_logprobs_bwd_workspace_bytes", [i64, i64, i64, i64, i32, i64, psz]),
+            ("kd_head_logprobs_bwd", [vp, vp, i32, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp,
+                                      vp, vp, vp, vp, sz, vp]),
             ("kd_clip_grads_workspace_bytes", [vp, i32, psz]),
             ("kd_clip_grads", [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp])):
         getattr(lib, name).argtypes = args
@@ -201,6 +207,128 @@ class _TokenLogprobs(torch.autograd.Function):
         return grad, None, None, None, None
 
 
+# ---- from hidden states ------------------------------------------------------------------
+def head_logprobs_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
+                                  dtype: int = kd.KD_BF16) -> int:
+    """Workspace bytes of ``head_logprobs``."""
+    out = ctypes.c_size_t(0)
+    kd._check(kd._lib().kd_head_logprobs_workspace_bytes(N, d, V, chunk, dtype, ctypes.byref(out)))
+    return int(out.value)
+
+
+def head_logprobs_bwd_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
+                                      dtype: int = kd.KD_BF16,
+                                      dw_group_tokens: int = 16384) -> int:
+    """Workspace bytes of ``head_logprobs_bwd``: for full speed, or for dW groups of at most
+    ``dw_group_tokens`` tokens (0: one chunk, the smallest accepted)."""
+    out = ctypes.c_size_t(0)
+    kd._check(kd._lib().kd_head_logprobs_bwd_workspace_bytes(N, d, V, chunk, dtype,
+                                                             dw_group_tokens, ctypes.byref(out)))
+    return int(out.value)
+
+
+def _head(h, W, tokens, **more):
+    kd._on_device(h.device, h=h, W=W, tokens=tokens, **more)
+    dt = kd._dtype_code(h)
+    if W.dtype != h.dtype:
+        raise TypeError("h and W must have the same dtype")
+    if h.dim() != 2 or W.dim() != 2 or W.shape[1] != h.shape[1]:
+        raise ValueError(f"h must be [N, d] and W [V, d], not {tuple(h.shape)}, {tuple(W.shape)}")
+    if not h.is_contiguous() or not W.is_contiguous():
+        raise ValueError("h and W must be contiguous")
+    N, d = h.shape
+    return dt, N, d, W.shape[0], _token_bits(tokens, N)
+
+
+def _head_logprobs(h, W, tokens, chunk, status, workspace, stats):
+    dt, N, d, V, bits = _head(h, W, tokens, status=status)
+    dev = h.device
+    workspace = _scratch(workspace, head_logprobs_workspace_bytes(N, d, V, chunk, dt), dev)
+    logp = torch.empty(N, dtype=_F32, device=dev)
+    entropy = torch.empty(N, dtype=_F32, device=dev)
+    lse = torch.empty(N, dtype=_F32, device=dev)
+    st = torch.empty((N, 2), dtype=_F32, device=dev) if stats else None
+    kd._check(kd._lib().kd_head_logprobs(
+        h.data_ptr(), W.data_ptr(), dt, tokens.data_ptr(), bits, N, d, V, chunk, logp.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), kd._ptr(st), _status_ptr(status),
+        workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream))
+    return (logp, entropy, lse), st
+
+
+def head_logprobs(h, W, tokens, chunk: int = 2048, status=None, workspace=None, stream=None):
+    """Log probabilities of given tokens from hidden states, with entropy and logsumexp:
+    ``token_logprobs`` of h W^T with no logits in memory.
+
+    Args (torch CUDA tensors, contiguous): h [N, d] and W [V, d], bfloat16 or float32 (same
+    dtype, d a multiple of 8); tokens [N] int32 or int64, negative where a row has no token;
+    chunk: token rows per pass; status, stream: as ``token_logprobs``; workspace: optional
+    uint8 tensor of ``head_logprobs_workspace_bytes`` bytes.
+    Returns (logp [N], entropy [N], lse [N]) float32, differentiable in h and W: the backward
+    recomputes the logits chunk by chunk."""
+    dev = h.device
+    kd._on_device(dev, h=h)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return head_logprobs(h, W, tokens, chunk, status, workspace)
+    if torch.is_grad_enabled() and (h.requires_grad or W.requires_grad):
+        return _HeadLogprobs.apply(h, W, tokens, chunk, status, workspace)
+    return _head_logprobs(h, W, tokens, chunk, status, workspace, False)[0]
+
+
+def head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp=None, grad_entropy=None,
+                      grad_lse=None, chunk: int = 2048, want_dh: bool = True,
+                      want_dW: bool = True, dw_group_tokens: int = 16384, workspace=None,
+                      stream=None):
+    """(dh [N, d] in h's dtype, dW [V, d] float32) of ``head_logprobs`` for upstream gradients
+    [N] of logp, entropy and lse (None: 0); None for the one that is not wanted.  ``row_stats``
+    [N, 2] and ``entropy`` [N] come from the forward; ``workspace`` and ``dw_group_tokens`` as
+    in ``fwd_bwd``."""
+    dev = h.device
+    kd._on_device(dev, h=h)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp, grad_entropy,
+                                     grad_lse, chunk, want_dh, want_dW, dw_group_tokens,
+                                     workspace)
+    dt, N, d, V, bits = _head(h, W, tokens, row_stats=row_stats, entropy=entropy)
+    _float_rows("row_stats", row_stats, (N, 2))
+    _float_rows("entropy", entropy, (N,))
+    g = [_upstream(n, x, N, dev) for n, x in (("grad_logp", grad_logp),
+                                              ("grad_entropy", grad_entropy),
+                                              ("grad_lse", grad_lse))]
+    workspace = _scratch(workspace, head_logprobs_bwd_workspace_bytes(
+        N, d, V, chunk, dt, dw_group_tokens) if workspace is None else 0, dev)
+    dh = torch.empty((N, d), dtype=h.dtype, device=dev) if want_dh else None
+    dW = torch.empty((V, d), dtype=_F32, device=dev) if want_dW else None
+    kd._check(kd._lib().kd_head_logprobs_bwd(
+        h.data_ptr(), W.data_ptr(), dt, tokens.data_ptr(), bits, N, d, V, chunk,
+        row_stats.data_ptr(), entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]),
+        kd._ptr(dh), kd._ptr(dW), workspace.data_ptr(), workspace.numel(),
+        torch.cuda.current_stream(dev).cuda_stream))
+    return dh, dW
+
+
+class _HeadLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, W, tokens, chunk, status, workspace):
+        ctx.set_materialize_grads(False)
+        outs, st = _head_logprobs(h, W, tokens, chunk, status, workspace, True)
+        ctx.save_for_backward(h, W, tokens, st, outs[1])
+        ctx.chunk = chunk
+        return outs
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_logp, g_entropy, g_lse):
+        h, W, tokens, st, entropy = ctx.saved_tensors
+        dh, dW = head_logprobs_bwd(h, W, tokens, st, entropy, g_logp, g_entropy, g_lse, ctx.chunk,
+                                   want_dh=ctx.needs_input_grad[0],
+                                   want_dW=ctx.needs_input_grad[1])
+        # dW is float32; autograd converts it to W's dtype if they differ
+        return dh, dW, None, None, None, None
+
+
+# ---- gradient norm and clipping -------------------------------------------------------------
 def _clip(grads, max_norm, out, workspace, stream):
     if not grads:
         raise ValueError("no tensors")

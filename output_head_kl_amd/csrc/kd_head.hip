@@ -1,0 +1,351 @@
+// Log probabilities of given tokens from hidden states, z = h W^T with no logits in memory,
+// and their gradients.  The products run on the MFMA GEMM core (kd_gemm.h) over one token
+// chunk at a time; these are its epilogues and the row kernels around it.
+//
+//  forward   per (token, wave row of the vocabulary tile): max, S = sum 2^t, T2 = sum t 2^t
+//            with t = (z - max) log2 e, and the given token's z straight from the lane that
+//            holds it; k_head_join folds the partials into logp, entropy and lse.
+//  gradient  z again, then dz = p (gz - gl - ge (ln p + H)) + gl [v = t] in one rounding, in
+//            the layouts the dh and dW GEMMs of the loss read.
+#include "kd_gemm.h"
+#include "kd_ops.h"
+
+namespace kd {
+namespace {
+
+// Tile rows are vocabulary entries v, columns tokens c (layouts as in kd_gemm.h).
+template <int DT>
+struct EpiHeadFwd {
+  static constexpr bool kPrefetch = false;
+  struct Pre {};
+  float2 *part;     // [n_lse][ld] (max, S)
+  float *part_t;    // [n_lse][ld] T2
+  long long ld;
+  int V, rows;
+  Tokens tokens;    // of the chunk
+  float *zt;        // [rows] the given tokens' logits
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void operator()(f32x16 (&acc)[NRB][NCB], int m0, int n0, int lane,
+                                             int, char *) const {
+    constexpr int WR = 32 * NRB;
+    if (m0 >= V) return;
+    const int vl = m0 + (lane >> 5) * 4;
+    const bool full = m0 + WR <= V;
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+      const int c = n0 + cb * 32 + (lane & 31);
+      const long long rel = c < rows ? tokens.at(c) - m0 : -1;  // the token's row in the wave
+      const int r = rel >= 0 && rel < WR && rel < V - m0 ? (int)rel : -1;
+      if (__builtin_amdgcn_ballot_w64(r >= 0)) {
+        // few waves hold a given token: the lane and accumulator with its row
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (rb * 32 + (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3) == r) zt[c] = acc[rb][cb][i];
+      }
+      float mx = -INFINITY;
+      if (full) {
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx = fmaxf(mx, acc[rb][cb][i]);
+      } else {
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (vl + rb * 32 + (i >> 2) * 8 + (i & 3) < V) mx = fmaxf(mx, acc[rb][cb][i]);
+      }
+      mx = halves_max(mx);
+      if (!full) {
+        // rows past the vocabulary: so far below the maximum that 2^t is 0, and finite
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (vl + rb * 32 + (i >> 2) * 8 + (i & 3) >= V) acc[rb][cb][i] = mx + kOpLowest;
+      }
+      const float mx2 = mx * kLog2e;
+      float s = 0.f, t2 = 0.f;
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float t = fmaf(acc[rb][cb][i], kLog2e, -mx2);
+          const float e = fast_exp2(t);
+          s += e;
+          t2 = fmaf(e, t, t2);
+        }
+      s = halves_sum(s);
+      t2 = halves_sum(t2);
+      if (lane < 32 && c < rows) {
+        part[(long long)(m0 / WR) * ld + c] = make_float2(mx, s);
+        part_t[(long long)(m0 / WR) * ld + c] = t2;
+      }
+    }
+  }
+};
+
+// 64 tokens per workgroup of 16 waves, lane = token: wave w folds the partials w, w + 16,
+// ..., wave 0 the 16 results, in a fixed order.
+constexpr int kJoinWaves = 16;
+__global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(const float2 *part,
+                                                               const float *part_t, int n_lse,
+                                                               long long ld, int rows, int V,
+                                                               const float *zt, Tokens tokens,
+                                                               LpOut out) {
+  __shared__ float sm[kJoinWaves][64];
+  __shared__ double sS[kJoinWaves][64], sT[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
+  float m = -3.4028234663852886e38f;
+  double S = 0.0, T = 0.0;
+  auto fold = [&](float m2, double S2, double T2) {
+    const float M = fmaxf(m, m2);
+    const float d1 = fmaxf(m - M, kOpLowest), d2 = fmaxf(m2 - M, kOpLowest);
+    const double c1 = (double)fast_exp2(d1 * kLog2e), c2 = (double)fast_exp2(d2 * kLog2e);
+    T = c1 * (T + (double)d1 * S) + c2 * (T2 + (double)d2 * S2);
+    S = c1 * S + c2 * S2;
+    m = M;
+  };
+  if (r < rows)
+    for (int t0 = w; t0 < n_lse; t0 += 4 * kJoinWaves) {
+      float2 q[4];
+      float t2[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u * kJoinWaves;
+        q[u] = t < n_lse ? part[t * ld + r] : make_float2(-INFINITY, 0.f);
+        t2[u] = t < n_lse ? part_t[t * ld + r] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (t0 + u * kJoinWaves < n_lse) fold(q[u].x, (double)q[u].y, kOpLn2d * (double)t2[u]);
+    }
+  sm[w][lane] = m;
+  sS[w][lane] = S;
+  sT[w][lane] = T;
+  __syncthreads();
+  if (w != 0 || r >= rows) return;
+#pragma unroll 1
+  for (int i = 1; i < kJoinWaves; ++i) fold(sm[i][lane], sS[i][lane], sT[i][lane]);
+  const long long tok = tokens.at(r);
+  lp_finish(out, r, m, S, T, tok, V, tok >= 0 && tok < V ? zt[r] : 0.f);
+}
+
+// Per token of a chunk, what the gradient's epilogue reads: l2 = lse log2 e, and dz =
+// p (a + b log2 p) + g [v = tok].
+__global__ void k_head_coef(Tokens tokens, LpGrad g, int rows, int V, float *l2, float *a,
+                            float *b, float *gt, int *tok32) {
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= rows) return;
+  const long long tok = tokens.at(r);
+  float gl = g.g_logp && tok >= 0 ? g.g_logp[r] : 0.f;
+  if (tok >= V) gl = __uint_as_float(0x7FC00000u);
+  const float ge = g.g_entropy ? g.g_entropy[r] : 0.f, gz = g.g_lse ? g.g_lse[r] : 0.f;
+  const float2 st = g.stats[r];
+  l2[r] = (float)(((double)st.x + (double)st.y) * 1.4426950408889634);
+  a[r] = (gz - gl) - ge * g.entropy[r];
+  b[r] = (float)(-(double)ge * kOpLn2d);
+  gt[r] = gl;
+  tok32[r] = tok >= 0 && tok < V ? (int)tok : -1;
+}
+
+template <int DT>
+struct EpiHeadDz {
+  static constexpr bool kPrefetch = false;
+  struct Pre {};
+  void *dz;      // blocks of 256 vocabulary columns: [V_pad/256][C_alloc][256]
+  long long ts;  // C_alloc * 256
+  const float *l2, *a, *b, *gt;
+  const int *tok;
+  int V, rows, V_pad;
+  unsigned short *dzt;  // bf16, or null: (v, c) at dzt[(c / 256) * tst + v * 256 + c % 256]
+  long long tst;
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void operator()(f32x16 (&acc)[NRB][NCB], int m0, int n0, int lane,
+                                             int, char *smem) const {
+    const int vl = m0 + (lane >> 5) * 4;
+    if (m0 + 32 * NRB > V) {
+      // rows V <= v < V_pad get p = 0 and a finite factor: dz = 0
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (vl + rb * 32 + (i >> 2) * 8 + (i & 3) >= V) {
+#pragma unroll
+            for (int cb = 0; cb < NCB; ++cb) acc[rb][cb][i] = -1e30f;
+          }
+    }
+    if constexpr (DT == 1) staged(acc, m0, n0, lane, smem);
+    else direct(acc, m0, n0, lane);
+  }
+
+  // One element: log2 p, p, then the formula; g is the given token's extra term or 0.
+  static __device__ __forceinline__ float one(float z, float l2, float a, float b, float g) {
+    const float q = fmaf(z, kLog2e, -l2);
+    return fmaf(fast_exp2(q), fmaf(b, q, a), g);
+  }
+
+  // fp32: four rows of a token at a time.
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void direct(const f32x16 (&acc)[NRB][NCB], int m0, int n0,
+                                         int lane) const {
+    const int vl = m0 + (lane >> 5) * 4;
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+      const int c = n0 + cb * 32 + (lane & 31);
+      if (c >= rows) continue;
+      const float cl2 = l2[c], ca = a[c], cbb = b[c], cg = gt[c];
+      const int ct = tok[c];
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int v0 = vl + rb * 32 + g * 8;
+          if (v0 >= V_pad) continue;  // V_pad is a multiple of 4
+          f32x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = one(acc[rb][cb][g * 4 + e], cl2, ca, cbb, v0 + e == ct ? cg : 0.f);
+          *(f32x4 *)((float *)dz + (long long)(v0 >> 8) * ts + c * 256 + (v0 & 255)) = x;
+        }
+    }
+  }
+
+  // bf16: through a per-wave LDS slice of [32 NCB tokens][64 rows] per pass, so that dz leaves
+  // as whole 128-byte lines of a token's rows and dzT as 16-byte pieces (8 tokens) of a row.
+  // The given token's element is written again in the slice, from its float32 value.
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void staged(const f32x16 (&acc)[NRB][NCB], int m0, int n0, int lane,
+                                         char *smem) const {
+    constexpr int RP = 2, NP = NRB / RP;                 // 32-row blocks per pass, passes
+    constexpr int TOK = 32 * NCB, PITCH = RP * 32 + 8;   // tokens per wave, bf16 per row
+    constexpr int QPR = RP * 32 / 8;                     // 16-byte pieces per token row
+    constexpr int TG = TOK / 8;                          // 8-token groups per vocabulary row
+    static_assert(NRB % RP == 0, "whole passes");
+    __syncthreads();  // every wave is done with the k-loop's LDS ring
+    LDS_AS unsigned short *stg =
+        (LDS_AS unsigned short *)smem + (threadIdx.x >> 6) * TOK * PITCH;
+    float cl2[NCB], ca[NCB], cbb[NCB], cg[NCB];
+    int ct[NCB];  // the given token's row in the wave, or out of range
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+      // tokens rows <= c < C_alloc get zeros: the dW GEMM reads dzT in 8-token chunks
+      const int c = n0 + cb * 32 + (lane & 31);
+      const bool cv = c < rows;
+      cl2[cb] = cv ? l2[c] : 0.f;
+      ca[cb] = cv ? a[c] : 0.f;
+      cbb[cb] = cv ? b[c] : 0.f;
+      cg[cb] = cv ? gt[c] : 0.f;
+      const int t = cv ? tok[c] : -1;
+      ct[cb] = t >= m0 && t - m0 < 32 * NRB ? t - m0 : -1;
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+#pragma unroll
+      for (int cb = 0; cb < NCB; ++cb) {
+        const int cl = cb * 32 + (lane & 31);
+#pragma unroll
+        for (int r = 0; r < RP; ++r)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = one(acc[p * RP + r][cb][g * 4 + e], cl2[cb], ca[cb], cbb[cb], 0.f);
+            const u32x2 pk = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+            *(LDS_AS u32x2 *)(stg + cl * PITCH + r * 32 + g * 8 + (lane >> 5) * 4) = pk;
+          }
+        const int hr = ct[cb] - p * RP * 32;
+        if (__builtin_amdgcn_ballot_w64(hr >= 0 && hr < RP * 32)) {
+#pragma unroll
+          for (int r = 0; r < RP; ++r)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int row = r * 32 + (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3);
+              if (row == hr)
+                stg[cl * PITCH + row] = f32_to_bf16(
+                    one(acc[p * RP + r][cb][i], cl2[cb], ca[cb], cbb[cb], cg[cb]));
+            }
+        }
+      }
+      const int vp = m0 + p * RP * 32;  // first vocabulary row of the pass
+#pragma unroll
+      for (int it = 0; it < TOK * QPR / 64; ++it) {
+        const int q = it * 64 + lane, cl = q / QPR, pc = q - cl * QPR;
+        const int c = n0 + cl, v = vp + pc * 8;
+        const u32x4 val = *(const LDS_AS u32x4 *)(stg + cl * PITCH + pc * 8);
+        if (c < rows && v < V_pad)
+          *(u32x4 *)((unsigned short *)dz + (long long)(v >> 8) * ts + c * 256 + (v & 255)) = val;
+      }
+      if (!dzt) continue;
+#pragma unroll
+      for (int it = 0; it < RP * 32 * TG / 64; ++it) {
+        const int q = it * 64 + lane, r = q / TG, tg = q - r * TG;
+        const int v = vp + r;
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = (unsigned)stg[(tg * 8 + 2 * e) * PITCH + r] |
+                 ((unsigned)stg[(tg * 8 + 2 * e + 1) * PITCH + r] << 16);
+        const int c = n0 + tg * 8;
+        if (v < V_pad)
+          __builtin_nontemporal_store(
+              o, (u32x4 *)(dzt + (long long)(c >> 8) * tst + (long long)v * 256 + (c & 255)));
+      }
+    }
+  }
+};
+
+}  // namespace
+
+hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
+                           int64_t V, const Tokens &tokens, float2 *part, float *part_t,
+                           int64_t ld_part, float *zt, hipStream_t s) {
+  Operand A{W, d, (int)V, (int)d, 256};
+  Operand B{h_c, d, (int)rows, (int)d, 256};
+  // token tiles in groups of eight: an XCD's concurrent workgroups then share four vocabulary
+  // tiles and eight token tiles
+  GemmGrid G{cdiv(V, tile_rows(dtype)), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
+  if (dtype == 1) {
+    EpiHeadFwd<1> e{part, part_t, ld_part, (int)V, (int)rows, tokens, zt};
+    return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
+  }
+  EpiHeadFwd<0> e{part, part_t, ld_part, (int)V, (int)rows, tokens, zt};
+  return run_gemm<0, OP_KC, OP_KC>(A, B, G, e, s);
+}
+
+hipError_t launch_head_join(const float2 *part, const float *part_t, int64_t n_lse,
+                            int64_t ld_part, int64_t rows, int64_t V, const float *zt,
+                            const Tokens &tokens, const LpOut &out, hipStream_t s) {
+  hipLaunchKernelGGL(k_head_join, dim3(cdiv(rows, 64)), dim3(64 * kJoinWaves), 0, s, part, part_t,
+                     (int)n_lse, (long long)ld_part, (int)rows, (int)V, zt, tokens, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows, int64_t V,
+                            const HeadCoef &k, hipStream_t s) {
+  hipLaunchKernelGGL(k_head_coef, dim3(cdiv(rows, 256)), dim3(256), 0, s, tokens, g, (int)rows,
+                     (int)V, k.l2, k.a, k.b, k.g, k.tok);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
+                          int64_t V, const HeadCoef &k, void *dz, void *dzt, int64_t tst,
+                          int64_t V_pad, int64_t C_alloc, hipStream_t s) {
+  // vocabulary tiles cover V_pad, so that dz holds zeros from V on
+  Operand A{W, d, (int)V, (int)d, 256};
+  Operand B{h_c, d, (int)rows, (int)d, 256};
+  GemmGrid G{(int)(V_pad / tile_rows(dtype)), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
+  if (dtype == 1) {
+    EpiHeadDz<1> e{dz, C_alloc * 256, k.l2, k.a, k.b, k.g, k.tok, (int)V, (int)rows, (int)V_pad,
+                   (unsigned short *)dzt, tst};
+    return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
+  }
+  EpiHeadDz<0> e{dz, C_alloc * 256, k.l2, k.a, k.b, k.g, k.tok, (int)V, (int)rows, (int)V_pad,
+                 nullptr, 0};
+  return run_gemm<0, OP_KC, OP_KC>(A, B, G, e, s);
+}
+
+}  // namespace kd

@@ -81,6 +81,25 @@ hipError_t launch_token_logprobs_bwd(int dtype, const void *logits, int64_t ld,
                                      const Tokens &tokens, int64_t N, int64_t V, const LpGrad &g,
                                      void *dlogits, int64_t ld_d, hipStream_t s);
 
+// --- log probabilities from hidden states (kd_head.hip), one token chunk per call ---
+// Partials per (wave row of the vocabulary tile, token): part = (max, S), part_t = T in base 2.
+hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
+                           int64_t V, const Tokens &tokens, float2 *part, float *part_t,
+                           int64_t ld_part, float *zt, hipStream_t s);
+hipError_t launch_head_join(const float2 *part, const float *part_t, int64_t n_lse,
+                            int64_t ld_part, int64_t rows, int64_t V, const float *zt,
+                            const Tokens &tokens, const LpOut &out, hipStream_t s);
+struct HeadCoef {  // per token of a chunk
+  float *l2, *a, *b, *g;
+  int *tok;
+};
+hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows, int64_t V,
+                            const HeadCoef &k, hipStream_t s);
+// dz in the layouts of launch_dh_gemm and launch_dw_gemm (dzt null: not wanted).
+hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
+                          int64_t V, const HeadCoef &k, void *dz, void *dzt, int64_t tst,
+                          int64_t V_pad, int64_t C_alloc, hipStream_t s);
+
 // --- gradient norm and clipping (kd_clip.hip) ---
 // Float64 partials of the squares' sum (one per chunk of a tensor).
 int64_t clip_partials(const int64_t *numel, int32_t n);

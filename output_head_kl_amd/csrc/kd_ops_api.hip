@@ -40,6 +40,56 @@ int check_logits(const void *logits, int32_t dtype, int64_t ld, const void *toke
   return KD_OK;
 }
 
+int check_head(const void *h, const void *W, int32_t dtype, const void *tokens, int32_t token_bits,
+               int64_t N, int64_t d, int64_t V, int64_t chunk, bool pointers) {
+  if (dtype != KD_F32 && dtype != KD_BF16) return set_error(KD_E_ARG, "dtype %d unknown", dtype);
+  if (N < 0 || d < 1 || V < 1) return set_error(KD_E_ARG, "need N >= 0, d >= 1, V >= 1");
+  if (chunk < 1) return set_error(KD_E_ARG, "chunk = %lld < 1", (long long)chunk);
+  if (d % 8 != 0)
+    return set_error(KD_E_UNSUPPORTED, "d = %lld is not a multiple of 8", (long long)d);
+  if (d > (1 << 20) || V > ((int64_t)1 << 24) || N > ((int64_t)1 << 40))
+    return set_error(KD_E_UNSUPPORTED, "d must be at most 2^20, V 2^24 and N 2^40");
+  if ((chunk < N ? chunk : N) > ((int64_t)1 << 22))
+    return set_error(KD_E_UNSUPPORTED, "min(chunk, N) must be at most 2^22 rows");
+  if (!pointers) return KD_OK;
+  if (token_bits != 32 && token_bits != 64)
+    return set_error(KD_E_ARG, "token_bits = %d: tokens are 32- or 64-bit integers", token_bits);
+  if (!W) return set_error(KD_E_ARG, "W is required");
+  if (N > 0 && (!h || !tokens)) return set_error(KD_E_ARG, "h and tokens are required when N > 0");
+  if (mis(h, 16) || mis(W, 16)) return set_error(KD_E_ARG, "h and W must be 16-byte aligned");
+  if (mis(tokens, token_bits / 8)) return set_error(KD_E_ARG, "tokens misaligned");
+  return KD_OK;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need) {
+  if (!workspace) return set_error(KD_E_WORKSPACE, "workspace is required (%zu bytes)", need);
+  if (mis(workspace, 256)) return set_error(KD_E_ARG, "workspace must be 256-byte aligned");
+  if (bytes < need)
+    return set_error(KD_E_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+  return KD_OK;
+}
+
+// Forward workspace: the partials of one chunk and its given tokens' logits.
+struct HeadFwd {
+  int64_t C, C_alloc, n_lse;
+  size_t off_t, off_zt, total;
+};
+HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
+  HeadFwd L;
+  L.C = chunk < N ? chunk : (N > 0 ? N : 1);
+  L.C_alloc = rup(L.C, 64);
+  const int64_t wr = kd::tile_rows(dtype) / 2;
+  L.n_lse = (V + wr - 1) / wr;
+  L.off_t = (size_t)rup(L.n_lse * L.C_alloc * 8, 256);
+  L.off_zt = L.off_t + (size_t)rup(L.n_lse * L.C_alloc * 4, 256);
+  L.total = L.off_zt + (size_t)rup(L.C_alloc * 4, 256);
+  return L;
+}
+
+kd::Tokens tokens_at(const void *tokens, int32_t token_bits, int64_t c0) {
+  return kd::Tokens{(const char *)tokens + c0 * (token_bits / 8), token_bits == 64};
+}
+
 int check_tensors(const int64_t *numel, int32_t n) {
   if (n < 0) return set_error(KD_E_ARG, "n = %d < 0", n);
   if (n > 0 && !numel) return set_error(KD_E_ARG, "numel is required when n > 0");
@@ -123,10 +173,8 @@ int kd_token_logprobs(const void *logits, int32_t dtype, int64_t ld, const void 
   if (mis(row_stats, 8)) return set_error(KD_E_ARG, "row_stats must be 8-byte aligned");
   const size_t need = kd::lp_workspace(N, V, top, dtype);
   if (need > 0) {
-    if (!workspace) return set_error(KD_E_WORKSPACE, "workspace is required (%zu bytes)", need);
-    if (mis(workspace, 256)) return set_error(KD_E_ARG, "workspace must be 256-byte aligned");
-    if (workspace_bytes < need)
-      return set_error(KD_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc != KD_OK) return rc;
   }
   if (N == 0) return KD_OK;
   hipStream_t stream = (hipStream_t)stream_v;
@@ -171,6 +219,140 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
   return KD_OK;
 }
 
+int kd_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
+                                     int32_t dtype, size_t *bytes_out) {
+  set_error(KD_OK, nullptr);
+  if (!bytes_out) return set_error(KD_E_ARG, "bytes_out is NULL");
+  int rc = check_head(nullptr, nullptr, dtype, nullptr, 0, N, d, V, chunk, false);
+  if (rc != KD_OK) return rc;
+  *bytes_out = head_fwd_layout(N, V, chunk, dtype).total;
+  return KD_OK;
+}
+
+int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *tokens,
+                     int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                     float *logp, float *entropy, float *row_lse, float *row_stats,
+                     int32_t *status, void *workspace, size_t workspace_bytes, void *stream_v) {
+  set_error(KD_OK, nullptr);
+  int rc = check_head(h, W, dtype, tokens, token_bits, N, d, V, chunk, true);
+  if (rc != KD_OK) return rc;
+  if (N > 0 && (!logp || !entropy || !row_lse))
+    return set_error(KD_E_ARG, "logp, entropy and row_lse are required when N > 0");
+  if (mis(logp, 4) || mis(entropy, 4) || mis(row_lse, 4) || mis(status, 4))
+    return set_error(KD_E_ARG, "outputs must be 4-byte aligned");
+  if (mis(row_stats, 8)) return set_error(KD_E_ARG, "row_stats must be 8-byte aligned");
+  const HeadFwd L = head_fwd_layout(N, V, chunk, dtype);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc != KD_OK) return rc;
+  hipStream_t stream = (hipStream_t)stream_v;
+  float2 *part = (float2 *)workspace;
+  float *part_t = (float *)((char *)workspace + L.off_t);
+  float *zt = (float *)((char *)workspace + L.off_zt);
+  const int64_t es = dtype == KD_BF16 ? 2 : 4;
+  for (int64_t c0 = 0; c0 < N; c0 += L.C) {
+    const int64_t rows = N - c0 < L.C ? N - c0 : L.C;
+    const char *h_c = (const char *)h + c0 * d * es;
+    const kd::Tokens tok = tokens_at(tokens, token_bits, c0);
+    LAUNCH(kd::KC_FWD_GEMM, kd::launch_head_fwd(dtype, W, h_c, rows, d, V, tok, part, part_t,
+                                                L.C_alloc, zt, stream));
+    const kd::LpOut out{logp + c0, entropy + c0, row_lse + c0,
+                        row_stats ? (float2 *)row_stats + c0 : nullptr, nullptr, nullptr, status,
+                        KD_E_INDEX};
+    LAUNCH(kd::KC_LOGPROBS, kd::launch_head_join(part, part_t, L.n_lse, L.C_alloc, rows, V, zt,
+                                                 tok, out, stream));
+  }
+  return KD_OK;
+}
+
+int kd_head_logprobs_bwd_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
+                                         int32_t dtype, int64_t dw_group_tokens,
+                                         size_t *bytes_out) {
+  set_error(KD_OK, nullptr);
+  if (!bytes_out) return set_error(KD_E_ARG, "bytes_out is NULL");
+  int rc = check_head(nullptr, nullptr, dtype, nullptr, 0, N, d, V, chunk, false);
+  if (rc != KD_OK) return rc;
+  if (dw_group_tokens < 0) return set_error(KD_E_ARG, "dw_group_tokens is negative");
+  if (dw_group_tokens > kd::kDwGroupTokens) dw_group_tokens = kd::kDwGroupTokens;
+  kd::Layout L;
+  kd::make_layout(N, d, V, 1, chunk, dtype, dw_group_tokens, &L);
+  *bytes_out = L.total;
+  return KD_OK;
+}
+
+int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void *tokens,
+                         int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                         const float *row_stats, const float *entropy, const float *grad_logp,
+                         const float *grad_entropy, const float *grad_lse, void *dh, float *dW,
+                         void *workspace, size_t workspace_bytes, void *stream_v) {
+  set_error(KD_OK, nullptr);
+  int rc = check_head(h, W, dtype, tokens, token_bits, N, d, V, chunk, true);
+  if (rc != KD_OK) return rc;
+  if (!dh && !dW) return set_error(KD_E_ARG, "neither dh nor dW is wanted");
+  if (N > 0 && (!row_stats || !entropy))
+    return set_error(KD_E_ARG, "row_stats and entropy are required when N > 0");
+  if (mis(row_stats, 8)) return set_error(KD_E_ARG, "row_stats must be 8-byte aligned");
+  if (mis(entropy, 4) || mis(grad_logp, 4) || mis(grad_entropy, 4) || mis(grad_lse, 4))
+    return set_error(KD_E_ARG, "float arguments must be 4-byte aligned");
+  if (mis(dh, 16) || mis(dW, 16)) return set_error(KD_E_ARG, "dh and dW must be 16-byte aligned");
+  // the dW group is the largest (up to kDwGroupTokens tokens) whose copies fit
+  kd::Layout L;
+  kd::make_layout(N, d, V, 1, chunk, dtype, kd::kDwGroupTokens, &L);
+  while (workspace_bytes < L.total && L.dw_group > 1)
+    kd::make_layout(N, d, V, 1, chunk, dtype, (int64_t)(L.dw_group - 1) * L.C_alloc, &L);
+  rc = check_workspace(workspace, workspace_bytes, L.total);
+  if (rc != KD_OK) return rc;
+  hipStream_t stream = (hipStream_t)stream_v;
+  if (N == 0) {
+    if (dW) LAUNCH(kd::KC_MISC, kd::launch_fill_zero(dW, (size_t)V * d * 4, stream));
+    return KD_OK;
+  }
+  char *ws = (char *)workspace;
+  const kd::HeadCoef k{(float *)(ws + L.off_lse), (float *)(ws + L.off_sM), (float *)(ws + L.off_s),
+                       (float *)(ws + L.off_zg), (int *)(ws + L.off_idxloc)};
+  void *dz = ws + L.off_dz, *WT = ws + L.off_wt;
+  const bool bf16 = dtype == KD_BF16, copies = bf16 && dW;  // token-contiguous dW operands
+  float *dhpart = (float *)(ws + L.off_dhpart);
+  const int64_t es = bf16 ? 2 : 4, tst_dz = L.V_pad * 256, tst_h = d * 256;
+  if (dh && bf16)
+    LAUNCH(kd::KC_TRANSPOSE, kd::launch_transpose_w(W, V, d, L.V_pad, WT, stream));
+  int chunk_i = 0, dw_launches = 0;
+  for (int64_t c0 = 0; c0 < N; c0 += L.C, ++chunk_i) {
+    const int64_t rows = N - c0 < L.C ? N - c0 : L.C;
+    const char *h_c = (const char *)h + c0 * d * es;
+    const kd::LpGrad g{(const float2 *)row_stats + c0, entropy + c0,
+                       grad_logp ? grad_logp + c0 : nullptr,
+                       grad_entropy ? grad_entropy + c0 : nullptr,
+                       grad_lse ? grad_lse + c0 : nullptr};
+    LAUNCH(kd::KC_LOGPROBS_BWD,
+           kd::launch_head_coef(tokens_at(tokens, token_bits, c0), g, rows, V, k, stream));
+    const int slot = chunk_i % L.dw_group;
+    void *dzt_c = copies ? ws + L.off_dzt + (size_t)slot * L.C_alloc * L.V_pad * 2 : nullptr;
+    LAUNCH(kd::KC_BWD_GEMM, kd::launch_head_dz(dtype, W, h_c, rows, d, V, k, dz, dzt_c, tst_dz,
+                                               L.V_pad, L.C_alloc, stream));
+    if (dh) {
+      LAUNCH(kd::KC_DH_GEMM, kd::launch_dh_gemm(dtype, dz, W, WT, rows, d, V, L.V_pad, L.nsplit,
+                                                L.k_split, dhpart, L.d_pad, L.C_alloc, stream));
+      LAUNCH(kd::KC_DH_REDUCE, kd::launch_dh_reduce(dtype, dhpart, L.nsplit, L.C_alloc, L.d_pad,
+                                                    rows, d, (char *)dh + c0 * d * es, stream));
+    }
+    if (!dW) continue;
+    void *ht = bf16 ? ws + L.off_ht : nullptr;
+    if (bf16)
+      LAUNCH(kd::KC_TRANSPOSE,
+             kd::launch_transpose_h(h_c, rows, d, L.C_alloc,
+                                    (char *)ht + (size_t)slot * L.C_alloc * d * 2, tst_h, stream));
+    if (slot == L.dw_group - 1 || c0 + rows >= N) {
+      // every earlier chunk of the group is whole: its columns past C are zero
+      const int64_t kk = (int64_t)slot * L.C_alloc + rows;
+      LAUNCH(kd::KC_DW_GEMM,
+             kd::launch_dw_gemm(dtype, dz, bf16 ? ws + L.off_dzt : nullptr, h_c, ht, kk, d, V,
+                                L.V_pad, L.C_alloc, dW, dw_launches > 0, stream));
+      ++dw_launches;
+    }
+  }
+  return KD_OK;
+}
+
 int kd_clip_grads_workspace_bytes(const int64_t *numel, int32_t n, size_t *bytes_out) {
   set_error(KD_OK, nullptr);
   if (!bytes_out) return set_error(KD_E_ARG, "bytes_out is NULL");
@@ -207,11 +389,9 @@ int kd_clip_grads(const void *const *grads, void *const *outs, const int64_t *nu
     }
     if (rc != KD_OK) return rc;
   }
-  const size_t need = (size_t)rup((kd::clip_partials(numel, n) + 1) * 8, 256);
-  if (!workspace) return set_error(KD_E_WORKSPACE, "workspace is required (%zu bytes)", need);
-  if (mis(workspace, 256)) return set_error(KD_E_ARG, "workspace must be 256-byte aligned");
-  if (workspace_bytes < need)
-    return set_error(KD_E_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  rc = check_workspace(workspace, workspace_bytes,
+                       (size_t)rup((kd::clip_partials(numel, n) + 1) * 8, 256));
+  if (rc != KD_OK) return rc;
   hipStream_t stream = (hipStream_t)stream_v;
   LAUNCH(kd::KC_CLIP, kd::launch_clip_grads(grads, outs, numel, dtypes, n, scale, max_norm, norm,
                                             (double *)workspace, stream));
