@@ -9,12 +9,19 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 namespace kd {
 namespace {
 
-constexpr int kLpThreads = 256, kLpWaves = kLpThreads / 64;
-constexpr int kLpSlots = 4;  // 16-byte loads in flight per thread and step
+#ifndef LP_NT
+#define LP_NT 256
+#endif
+#ifndef LP_U
+#define LP_U 4
+#endif
+constexpr int kLpThreads = LP_NT;
+constexpr int kLpSlots = LP_U;  // 16-byte loads in flight per thread and step
 
 template <int DT> struct LpT;
 template <> struct LpT<1> { static constexpr int EPL = 8, ES = 2; };
@@ -74,87 +81,164 @@ __device__ __forceinline__ float key_val(unsigned k) {
 __device__ __forceinline__ uint64_t sel_key(float x, unsigned idx) {
   return ((uint64_t)val_key(x) << 32) | (unsigned)~idx;
 }
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) {
-  const unsigned lo = __shfl_xor((unsigned)v, o, 64), hi = __shfl_xor((unsigned)(v >> 32), o, 64);
-  return ((uint64_t)hi << 32) | lo;
+
+// The value of lane ^ J, J a power of two: data-parallel moves inside 16 lanes, row and half
+// swaps beyond, so that a sorting stage waits a few cycles instead of an LDS round trip.
+template <int J>
+__device__ __forceinline__ unsigned lane_xor(unsigned v, int lane) {
+  if constexpr (J == 1) return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xF, 0xF, true);
+  else if constexpr (J == 2) return __builtin_amdgcn_update_dpp(0u, v, 0x4E, 0xF, 0xF, true);
+  else if constexpr (J == 4) {  // reversed in eights, then in fours
+    const unsigned r = __builtin_amdgcn_update_dpp(0u, v, 0x141, 0xF, 0xF, true);
+    return __builtin_amdgcn_update_dpp(0u, r, 0x1B, 0xF, 0xF, true);
+  } else if constexpr (J == 8) return __builtin_amdgcn_update_dpp(0u, v, 0x128, 0xF, 0xF, true);
+  else if constexpr (J == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (lane & 16) ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (lane & 32) ? r[0] : r[1];
+  }
+}
+template <int J>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int lane) {
+  return ((uint64_t)lane_xor<J>((unsigned)(v >> 32), lane) << 32) | lane_xor<J>((unsigned)v, lane);
+}
+// One stage: lanes with keep_max keep the larger of the pair.
+template <int J, class K>
+__device__ __forceinline__ K sort_stage(K v, int lane, bool keep_max) {
+  const K o = lane_xor<J>(v, lane);
+  return (v > o) == keep_max ? v : o;
+}
+template <int J, class K>
+__device__ __forceinline__ K sort_down(K v, int lane, bool desc) {
+  v = sort_stage<J>(v, lane, ((lane & J) == 0) == desc);
+  if constexpr (J > 1) v = sort_down<J / 2>(v, lane, desc);
+  return v;
+}
+// Bitonic sort of the wave's 64 keys, descending over the lanes.
+template <class K>
+__device__ __forceinline__ K wave_sort(K v, int lane) {
+  v = sort_down<1>(v, lane, (lane & 2) == 0);
+  v = sort_down<2>(v, lane, (lane & 4) == 0);
+  v = sort_down<4>(v, lane, (lane & 8) == 0);
+  v = sort_down<8>(v, lane, (lane & 16) == 0);
+  v = sort_down<16>(v, lane, (lane & 32) == 0);
+  return sort_down<32>(v, lane, true);
 }
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int l) {
   const unsigned lo = __shfl((unsigned)v, l, 64), hi = __shfl((unsigned)(v >> 32), l, 64);
   return ((uint64_t)hi << 32) | lo;
 }
-// Bitonic sort of the wave's 64 keys, descending over the lanes.
-template <class K, class X>
-__device__ __forceinline__ K wave_sort(K v, int lane, X xchg) {
-#pragma unroll
-  for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const K o = xchg(v, j);
-      const bool keep_max = ((lane & k) == 0) == ((lane & j) == 0);
-      v = keep_max ? (v > o ? v : o) : (v < o ? v : o);
-    }
-  return v;
-}
 // The 64 largest of two descending lists, descending.
 __device__ __forceinline__ uint64_t wave_merge(uint64_t a, uint64_t b, int lane) {
   const uint64_t r = shfl64(b, 63 - lane);
-  uint64_t v = a > r ? a : r;  // bitonic
-#pragma unroll
-  for (int j = 32; j > 0; j >>= 1) {
-    const uint64_t o = shfl_xor64(v, j);
-    v = (lane & j) == 0 ? (v > o ? v : o) : (v < o ? v : o);
+  return sort_down<32>(a > r ? a : r, lane, true);  // the larger ones are bitonic
+}
+// Of n keys in LDS, any order, the 64 largest, descending.
+__device__ __forceinline__ uint64_t wave_best(const volatile uint64_t *keys, int n, int lane) {
+  uint64_t list = 0;
+  for (int i = 0; i < n; i += 64) {
+    const uint64_t v = wave_sort(i + lane < n ? keys[i + lane] : (uint64_t)0, lane);
+    list = i == 0 ? v : wave_merge(list, v, lane);
   }
-  return v;
+  return list;
 }
 
-// A wave's running list of its 64 largest keys (one per lane, descending) with a buffer of
-// candidates in LDS.  An element is a candidate if it reaches the threshold: the `top`-th
-// largest so far (strictly above it once its slot is done: later elements of the wave have
-// larger indices), or another wave's `top`-th value.
-constexpr int kLpBuf = 128;
+// A wave's candidates for the row's `top` largest.  The streaming loop only notes, in LDS,
+// which groups of elements hold one (a compare of the group's maximum and a few instructions
+// where it passes); the groups are read again when a wave's worth of them has come together,
+// which is a few dozen of a row's thousands.
+// An element is a candidate if it is above the threshold, or equal to it with an index below
+// `tie`.  Every threshold is a value that at least `top` elements of the row reach: the top-th
+// largest of the 64 lanes' maxima, another wave's threshold (ties are let in), or, where the
+// buffer was cut back to its largest, the top-th of those (ties with a larger index are not).
+constexpr int kLpBuf = 256;   // keys of candidates per wave
+constexpr int kLpNotes = 384; // noted groups per wave: room for a whole step is kept
 struct WaveTop {
-  uint64_t list;
   float thr;
-  int cnt, top, lane;
+  unsigned tie;
+  int cnt, notes, top, lane;
   volatile uint64_t *buf;
-  __device__ __forceinline__ void init(int top_, int lane_, volatile uint64_t *b) {
-    list = 0;
+  volatile unsigned *note;
+  __device__ __forceinline__ void init(int top_, int lane_, volatile uint64_t *b,
+                                       volatile unsigned *n) {
     thr = -INFINITY;
-    cnt = 0;
+    tie = ~0u;
+    cnt = notes = 0;
     top = top_;
     lane = lane_;
     buf = b;
+    note = n;
   }
-  __device__ __forceinline__ void flush() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    while (cnt > 0) {
-      const int n = cnt < 64 ? cnt : 64;
-      uint64_t v = lane < n ? buf[cnt - n + lane] : 0ull;
-      v = wave_sort(v, lane, [](uint64_t x, int o) { return shfl_xor64(x, o); });
-      list = wave_merge(list, v, lane);
-      cnt -= n;
+  __device__ __forceinline__ void raise(float v) {
+    if (v > thr) {
+      thr = v;
+      tie = ~0u;
     }
+  }
+  __device__ __forceinline__ void cut() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const uint64_t list = wave_best(buf, cnt, lane);
+    cnt = __popcll(__builtin_amdgcn_ballot_w64(list != 0 && lane < top));
+    if (lane < cnt) buf[lane] = list;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const unsigned hi = __builtin_amdgcn_readlane((unsigned)(list >> 32), top - 1);
+    const unsigned lo = __builtin_amdgcn_readlane((unsigned)list, top - 1);
+    if (hi != 0 && key_val(hi) >= thr) {
+      thr = key_val(hi);
+      tie = ~lo;
+    }
   }
-  // The top-th value so far, -inf if there are fewer; strict: the next float above it.
-  __device__ __forceinline__ void raise(bool strict) {
-    const unsigned k = __builtin_amdgcn_readfirstlane(__shfl((unsigned)(list >> 32), top - 1, 64));
-    if (k != 0) thr = fmaxf(thr, key_val(strict ? k + 1 : k));
+  __device__ __forceinline__ bool above(float x, unsigned idx) const {
+    return x > thr || (x == thr && idx < tie);
   }
-  __device__ __forceinline__ void offer(float x, unsigned idx, bool valid) {
-    uint64_t mask = __builtin_amdgcn_ballot_w64(valid && x >= thr);
+  // Lanes below this one in the mask.
+  static __device__ __forceinline__ int prefix(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32),
+                                     __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0));
+  }
+  // Notes the group at index idx whose maximum is mx, if it can hold a candidate.
+  __device__ __forceinline__ void look(float mx, unsigned idx) {
+    const bool in = above(mx, idx);
+    const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
     if (mask == 0) return;
-    if (cnt + __popcll(mask) > kLpBuf) {  // then the list is emptied, and at most 64 come in
-      flush();
-      raise(false);
-      mask = __builtin_amdgcn_ballot_w64(valid && x >= thr);
+    if (in) note[notes + prefix(mask)] = idx;
+    notes += __popcll(mask);
+  }
+  // Reads the noted groups (at: from index to address; end: the range's) and keeps their
+  // candidates.
+  template <int DT, class At>
+  __device__ __forceinline__ void drain(unsigned end, At at) {
+    constexpr int EPL = LpT<DT>::EPL;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int i = 0;; i += 64) {
+      const bool has = i + lane < notes, done = i >= notes;
+      const unsigned e = has ? note[i + lane] : 0u;
+      // a group at the end is read from the last whole group's place: skip what precedes it
+      const unsigned from = has && e + EPL <= end ? e : end - EPL;
+      u4 r = load16(at(from));
+#pragma unroll 1
+      for (int j = 0; j < EPL; ++j) {
+        // room for 64 more; at the end no more than 64
+        if (cnt > (done ? 64 : kLpBuf - 64)) cut();
+        if (done) break;
+        const float x = __uint_as_float(DT == 0 ? r[0] : r[0] << 16);
+        const bool in = has && from + j >= e && above(x, from + j);
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+        if (in) buf[cnt + prefix(mask)] = sel_key(x, from + j);
+        cnt += __popcll(mask);
+        if (DT == 0) {
+          r = u4{r[1], r[2], r[3], 0u};
+        } else {
+          r = u4{(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
+                 (r[2] >> 16) | (r[3] << 16), r[3] >> 16};
+        }
+      }
+      if (done) break;
     }
-    if ((mask >> lane) & 1) {
-      const int at = cnt + __builtin_amdgcn_mbcnt_hi((unsigned)(mask >> 32),
-                                                     __builtin_amdgcn_mbcnt_lo((unsigned)mask, 0));
-      buf[at] = sel_key(x, idx);
-    }
-    cnt += __popcll(mask);
+    notes = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 };
 
@@ -165,16 +249,26 @@ struct LpPart {
   int pad;
 };
 
-// Joins (m2, S2, T2) to (m, S, T).  No value yet: m = -FLT_MAX, S = T = 0.
+constexpr float kLpNone = -3.4028234663852886e38f;  // m before the first value
+
+// Joins (m2, S2, T2) to (m, S, T).
 __device__ __forceinline__ void lp_join(float &m, double &S, double &T, float m2, double S2,
                                         double T2) {
-  const float M = fmaxf(m, m2);
+  const float M = __builtin_elementwise_maximum(m, m2);  // NaN stays
   const float d1 = fmaxf(m - M, kOpLowest), d2 = fmaxf(m2 - M, kOpLowest);
   const double c1 = (double)__builtin_amdgcn_exp2f(d1 * kOpLog2e);
   const double c2 = (double)__builtin_amdgcn_exp2f(d2 * kOpLog2e);
   T = c1 * (T + (double)d1 * S) + c2 * (T2 + (double)d2 * S2);
   S = c1 * S + c2 * S2;
   m = M;
+}
+__device__ __forceinline__ void wave_join(float &m, double &S, double &T) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor(m, o, 64);
+    const double S2 = __shfl_xor(S, o, 64), T2 = __shfl_xor(T, o, 64);
+    lp_join(m, S, T, m2, S2, T2);
+  }
 }
 
 struct LpArgs {
@@ -190,60 +284,98 @@ struct LpArgs {
 
 // The row's alternatives from the sorted list (lane k holds the k-th).
 __device__ __forceinline__ void write_top(const LpOut &o, long long row, int top, int lane,
-                                          uint64_t key, float m, double lnS) {
+                                          uint64_t key, float m, float lnS) {
   if (lane >= top) return;
   const float nan = __uint_as_float(0x7FC00000u);
-  const bool bad = lnS != lnS, empty = lnS == -(double)INFINITY;
+  const bool bad = lnS != lnS, empty = lnS == -INFINITY;
   const float x = key_val((unsigned)(key >> 32));
   o.top_idx[row * top + lane] = bad ? -1 : (int32_t)~(unsigned)key;
-  o.top_logp[row * top + lane] =
-      bad ? nan : empty ? -INFINITY : (float)((double)x - (double)m - lnS);
+  o.top_logp[row * top + lane] = bad ? nan : empty ? -INFINITY : (x - m) - lnS;
 }
 
-// One workgroup per (row, vocabulary split).
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void k_token_logprobs(LpArgs a) {
-  constexpr int EPL = LpT<DT>::EPL, U = kLpSlots;
-  __shared__ float s_m[kLpWaves];
-  __shared__ double s_S[kLpWaves], s_T[kLpWaves];
-  __shared__ volatile float s_thr[kLpWaves];
-  __shared__ uint64_t s_buf[TOP ? kLpWaves * kLpBuf : 1];
+template <int DT>
+__device__ __forceinline__ float logit_at(const char *row, long long v) {
+  return DT == 0 ? ((const float *)row)[v]
+                 : __uint_as_float((unsigned)((const unsigned short *)row)[v] << 16);
+}
+
+// One workgroup of NT threads per (row, vocabulary split).  A step is U 16-byte groups per
+// thread, loaded one step ahead.  Past the end a group is loaded from the range's last 16
+// bytes instead and what earlier groups hold is masked, so no load is conditional or leaves
+// the range (of at least one group).
+#ifndef LP_WAVES
+#define LP_WAVES 1
+#endif
+template <int DT, bool TOP, int NT>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) void k_token_logprobs(LpArgs a) {
+  constexpr int EPL = LpT<DT>::EPL, ES = LpT<DT>::ES, U = kLpSlots, NW = NT / 64;
+  __shared__ float s_m[NW], s_thr[NW];
+  __shared__ double s_S[NW], s_T[NW];
+  __shared__ uint64_t s_buf[TOP ? NW * kLpBuf : 1], s_pool[TOP ? NW * 64 : 1];
+  __shared__ unsigned s_note[TOP ? NW * kLpNotes : 1];
+  __shared__ int s_n;
 
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const long long row = blockIdx.x / a.S;
-  const int split = (int)(blockIdx.x - row * a.S);
-  const long long e0 = split * a.per, end = e0 + a.per < a.V ? e0 + a.per : a.V;
-  const char *rp = (const char *)a.logits + row * a.ld * LpT<DT>::ES;
+  const unsigned row = blockIdx.x / a.S, split = blockIdx.x - row * a.S;
+  const char *rp = (const char *)a.logits + row * a.ld * ES;
+  const long long e0 = split * a.per;
+  const int len = (int)(e0 + a.per < a.V ? a.per : a.V - e0);  // below 2^29
+  const char *sp = rp + e0 * ES;
   long long tok = -1;
   float zt = 0.f;
   if (t == 0 && a.S == 1) {
     tok = a.tokens.at(row);
-    if (tok >= 0 && tok < a.V)
-      zt = DT == 0 ? ((const float *)rp)[tok]
-                   : __uint_as_float((unsigned)((const unsigned short *)rp)[tok] << 16);
+    if (tok >= 0 && tok < a.V) zt = logit_at<DT>(rp, tok);
   }
 
-  float m = -3.4028234663852886e38f;
+  float m = kLpNone;
   double S = 0.0, T = 0.0;
   WaveTop wt;
+  int fresh = 0;  // groups noted since the wave's threshold was last renewed
+  volatile float *thr_of = s_thr;
   if (TOP) {
-    wt.init(a.top, lane, s_buf + w * kLpBuf);
-    if (lane == 0) s_thr[w] = -INFINITY;
+    wt.init(a.top, lane, s_buf + w * kLpBuf, s_note + w * kLpNotes);
+    if (t < NW) s_thr[t] = -INFINITY;
+    if (t == 0) s_n = 0;
     __syncthreads();
   }
-  bool first = true;
-  auto take = [&](const u4 (&raw)[U], long long base) {
-    float x[U][EPL];
-    float lu[U];
+
+  const unsigned last = (unsigned)(len - EPL) * ES;
+  auto load = [&](u4 (&r)[U], int step) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const unsigned off = ((unsigned)(step * U + u) * NT + t) * 16u;
+      r[u] = load16(sp + (off < last ? off : last));
+    }
+  };
+  float lu[U];  // the maxima of the step's groups, NaN where a group holds nothing new
+  // whole: every element of the step's groups is inside the range
+  auto take = [&](const u4 (&raw)[U], int step, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    float x[U][EPL], lm = -INFINITY;  // the maximum of all, NaN if an element is
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       unpack<DT>(raw[u], x[u]);
+      if (!WHOLE && (step * U + u) * NT * EPL >= len) {  // the same for the workgroup
+        lu[u] = NAN;
+        continue;
+      }
+      int first = 0;  // of the group's elements, those from here on are new
+      if (!WHOLE) {
+        const int e = ((step * U + u) * NT + t) * EPL;
+        first = e <= len - EPL ? 0 : e - (len - EPL);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if (j < first) x[u][j] = -INFINITY;
+      }
       lu[u] = x[u][0];
 #pragma unroll
-      for (int j = 1; j < EPL; ++j) lu[u] = fmaxf(lu[u], x[u][j]);
+      for (int j = 1; j < EPL; ++j) lu[u] = __builtin_elementwise_maximum(lu[u], x[u][j]);
+      lm = __builtin_elementwise_maximum(lm, lu[u]);
+      if (!WHOLE && first >= EPL) lu[u] = NAN;
     }
-    const float lm = fmaxf(fmaxf(lu[0], lu[1]), fmaxf(lu[2], lu[3]));
-    if (lm > m) {
+    if (!(lm <= m)) {  // also where the lane has met a NaN, which then stays
+      lm = __builtin_elementwise_maximum(lm, m);
       const float d = fmaxf(m - lm, kOpLowest);
       const double c = (double)__builtin_amdgcn_exp2f(d * kOpLog2e);
       T = c * (T + (double)d * S);
@@ -252,143 +384,142 @@ __global__ __launch_bounds__(kLpThreads) void k_token_logprobs(LpArgs a) {
     }
     float ps = 0.f, pt = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      if (!WHOLE && (step * U + u) * NT * EPL >= len) continue;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const float d = x[u][j] - m;
+        const float d = fmaxf(x[u][j] - m, kOpLowest);
         const float e = __builtin_amdgcn_exp2f(d * kOpLog2e);
         ps += e;
-        pt = fmaf(e, fmaxf(d, kOpLowest), pt);
-      }
-    S += (double)ps;
-    T += (double)pt;
-    if (TOP) {
-      if (first) {
-        // the top-th largest of the 64 lanes' maxima: at least `top` elements reach it
-        const unsigned k = wave_sort(val_key(lm), lane, [](unsigned v, int o) {
-          return (unsigned)__shfl_xor(v, o, 64);
-        });
-        wt.thr = key_val(__builtin_amdgcn_readfirstlane(__shfl(k, a.top - 1, 64)));
-        first = false;
-      }
-#pragma unroll
-      for (int i = 0; i < kLpWaves; ++i) wt.thr = fmaxf(wt.thr, s_thr[i]);
-      if (__builtin_amdgcn_ballot_w64(lm >= wt.thr)) {
-        for (int u = 0; u < U; ++u) {
-          if (!__builtin_amdgcn_ballot_w64(lu[u] >= wt.thr)) continue;
-          const long long e = base + ((long long)u * kLpThreads + t) * EPL;
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) wt.offer(x[u][j], (unsigned)(e + j), e + j < end);
-        }
-        if (wt.cnt >= 64) {
-          wt.flush();
-          wt.raise(false);
-          if (lane == 0) s_thr[w] = wt.thr;
-          wt.raise(true);
-        }
+        pt = fmaf(e, d, pt);
       }
     }
+    S += (double)ps;
+    T += (double)pt;
+  };
+  // The step's groups among the candidates; code that is kept in one place, as it is long and
+  // seldom runs.
+  auto choose = [&](int step, bool end) {
+    if (step == 0 || fresh >= 16) {  // the lanes' maxima have grown since the last look
+      const unsigned k = wave_sort(val_key(m > kLpNone ? m : -INFINITY), lane);
+      wt.raise(key_val(__builtin_amdgcn_readlane(k, a.top - 1)));
+      if (lane == 0) thr_of[w] = wt.thr;
+      fresh = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) wt.raise(thr_of[i]);
+    const int before = wt.notes;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      wt.look(lu[u], (unsigned)e0 + ((step * U + u) * NT + t) * EPL);
+    fresh += wt.notes - before;
+    if (wt.notes > kLpNotes - 64 * U || end)
+      wt.template drain<DT>((unsigned)e0 + len, [&](unsigned i) { return rp + (size_t)i * ES; });
   };
 
-  // Whole steps are loaded one step ahead; the rest of the range is loaded with tests.
-  constexpr long long STEP = (long long)kLpThreads * U * EPL;
-  const long long whole = (end - e0) / STEP;
-  u4 cur[U], nxt[U];
-  const char *tp = rp + (e0 + (long long)t * EPL) * LpT<DT>::ES;
-  if (whole > 0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) cur[u] = load16(tp + (size_t)u * kLpThreads * 16);
-    for (long long i = 0; i < whole; ++i) {
-      const long long n = i + 1 < whole ? i + 1 : i;  // the last step is loaded twice
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        nxt[u] = load16(tp + (n * U + u) * (long long)(kLpThreads * 16));
-      take(cur, e0 + i * STEP);
+  if (len >= EPL) {
+    constexpr int STEP = NT * U * EPL;
+    const int whole = len / STEP, steps = (len + STEP - 1) / STEP;
+    u4 cur[U], nxt[U];
+    load(cur, 0);
+    for (int i = 0; i < steps; ++i) {
+      load(nxt, i + 1);
+      if (i < whole) take(cur, i, std::true_type());
+      else take(cur, i, std::false_type());
+      if (TOP) choose(i, i + 1 == steps);
 #pragma unroll
       for (int u = 0; u < U; ++u) cur[u] = nxt[u];
     }
-  }
-  const long long rest = e0 + whole * STEP;
-  if (rest < end) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      cur[u] = load_group<DT>(rp, rest + ((long long)u * kLpThreads + t) * EPL, end);
-    take(cur, rest);
+  } else if (w == 0) {  // fewer elements than one group: one per lane
+    float x = -INFINITY;
+    if (lane < len) x = logit_at<DT>(sp, lane);
+    m = x > kLpNone || x != x ? x : kLpNone;
+    S = x == -INFINITY ? 0.0 : 1.0;
+    if (TOP) {
+      if (lane < len) wt.buf[lane] = sel_key(x, (unsigned)e0 + lane);
+      wt.cnt = len;
+    }
   }
 
-  // lanes, then waves
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor(m, o, 64);
-    const double S2 = __shfl_xor(S, o, 64), T2 = __shfl_xor(T, o, 64);
-    lp_join(m, S, T, m2, S2, T2);
-  }
+  wave_join(m, S, T);
   if (lane == 0) {
     s_m[w] = m;
     s_S[w] = S;
     s_T[w] = T;
-  }
-  if (TOP) {
-    wt.flush();
-    s_buf[w * kLpBuf + lane] = wt.list;
+    if (TOP) s_thr[w] = wt.thr;
   }
   __syncthreads();
-  if (w != 0) return;
-  for (int i = 1; i < kLpWaves; ++i) {
-    lp_join(m, S, T, s_m[i], s_S[i], s_T[i]);
-    if (TOP) wt.list = wave_merge(wt.list, s_buf[i * kLpBuf + lane], lane);
-  }
-  if (a.S > 1) {
-    const long long at = row * a.S + split;
-    if (lane == 0) a.part[at] = LpPart{S, T, m, 0};
-    if (TOP && lane < a.top) a.keys[at * a.top + lane] = wt.list;
-    return;
-  }
-  double lnS = 0.0;
-  if (lane == 0) lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
-  if (TOP) write_top(a.out, row, a.top, lane, wt.list, m, __shfl(lnS, 0, 64));
-}
-
-// Joins a row's vocabulary splits: one workgroup per row.
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void k_token_logprobs_join(LpArgs a) {
-  __shared__ uint64_t s_list[TOP ? kLpThreads : 1];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const long long row = blockIdx.x;
-  uint64_t list = 0;
   if (TOP) {
-    for (int i = w; i < a.S; i += kLpWaves) {
-      const uint64_t v = lane < a.top ? a.keys[(row * a.S + i) * a.top + lane] : 0ull;
-      list = wave_merge(list, v, lane);
-    }
-    s_list[t] = list;
+    // the waves' candidates that reach the best threshold, at most 64 of each
+    float thr = s_thr[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) thr = fmaxf(thr, s_thr[i]);
+    const uint64_t key = lane < wt.cnt ? wt.buf[lane] : 0;
+    const bool in = key != 0 && key_val((unsigned)(key >> 32)) >= thr;
+    if (in) s_pool[atomicAdd(&s_n, 1)] = key;
     __syncthreads();
   }
   if (w != 0) return;
-  if (TOP)
-    for (int i = 1; i < kLpWaves; ++i) list = wave_merge(list, s_list[i * 64 + lane], lane);
-  float m = -3.4028234663852886e38f;
+  for (int i = 1; i < NW; ++i) lp_join(m, S, T, s_m[i], s_S[i], s_T[i]);
+  uint64_t list = 0;
+  if (TOP) list = wave_best(s_pool, s_n, lane);
+  if (a.S > 1) {
+    const long long at = (long long)row * a.S + split;
+    if (lane == 0) a.part[at] = LpPart{S, T, m, 0};
+    if (TOP && lane < a.top) a.keys[at * a.top + lane] = list;
+    return;
+  }
+  float lnS = 0.f;
+  if (lane == 0) lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
+  if (TOP) write_top(a.out, row, a.top, lane, list, m, __shfl(lnS, 0, 64));
+}
+
+// Joins a row's vocabulary splits: one workgroup per row.
+constexpr int kLpMaxSplits = 64;
+template <int DT, bool TOP>
+__global__ __launch_bounds__(kLpThreads) void k_token_logprobs_join(LpArgs a) {
+  constexpr int NW = kLpThreads / 64;
+  __shared__ uint64_t s_thr[NW], s_pool[TOP ? kLpMaxSplits * kLpMaxTop : 1];
+  __shared__ int s_n;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const long long row = blockIdx.x;
+  float m = kLpNone, zt = 0.f;
   double S = 0.0, T = 0.0;
-  for (int i = lane; i < a.S; i += 64) {
-    const LpPart p = a.part[row * a.S + i];
-    lp_join(m, S, T, p.m, p.S, p.T);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor(m, o, 64);
-    const double S2 = __shfl_xor(S, o, 64), T2 = __shfl_xor(T, o, 64);
-    lp_join(m, S, T, m2, S2, T2);
-  }
-  double lnS = 0.0;
-  if (lane == 0) {
-    const long long tok = a.tokens.at(row);
-    float zt = 0.f;
-    const char *rp = (const char *)a.logits + row * a.ld * LpT<DT>::ES;
+  long long tok = -1;
+  if (w == 0) {
+    if (lane < a.S) {
+      const LpPart p = a.part[row * a.S + lane];
+      m = p.m;
+      S = p.S;
+      T = p.T;
+    }
+    tok = a.tokens.at(row);
     if (tok >= 0 && tok < a.V)
-      zt = DT == 0 ? ((const float *)rp)[tok]
-                   : __uint_as_float((unsigned)((const unsigned short *)rp)[tok] << 16);
-    lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
+      zt = logit_at<DT>((const char *)a.logits + row * a.ld * LpT<DT>::ES, tok);
   }
+  if (TOP) {
+    // the top-th largest of a wave's 64 lane maxima bounds the row's top-th key from below
+    const uint64_t *k = a.keys + row * a.S * a.top;
+    const int n = a.S * a.top;
+    uint64_t best = 0;
+    for (int i = t; i < n; i += kLpThreads) best = k[i] > best ? k[i] : best;
+    best = wave_sort(best, lane);
+    if (lane == a.top - 1) s_thr[w] = best;
+    if (t == 0) s_n = 0;
+    __syncthreads();
+    uint64_t thr = s_thr[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) thr = s_thr[i] > thr ? s_thr[i] : thr;
+    for (int i = t; i < n; i += kLpThreads)
+      if (k[i] != 0 && k[i] >= thr) s_pool[atomicAdd(&s_n, 1)] = k[i];
+    __syncthreads();
+  }
+  if (w != 0) return;
+  wave_join(m, S, T);
+  uint64_t list = 0;
+  if (TOP) list = wave_best(s_pool, s_n, lane);
+  float lnS = 0.f;
+  if (lane == 0) lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
   if (TOP) write_top(a.out, row, a.top, lane, list, m, __shfl(lnS, 0, 64));
 }
 
@@ -471,7 +602,7 @@ inline int64_t cd(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int lp_splits(int64_t N, int64_t V, int) {
   const int64_t want = N > 0 ? 1024 / N : 1, most = cd(V, 4096);
   int64_t s = want < most ? want : most;
-  if (s > 64) s = 64;
+  if (s > kLpMaxSplits) s = kLpMaxSplits;
   return s < 1 ? 1 : (int)s;
 }
 
@@ -480,31 +611,38 @@ size_t lp_workspace(int64_t N, int64_t V, int32_t top, int dtype) {
   return S == 1 ? 0 : (size_t)(N * S) * (sizeof(LpPart) + 8 * (size_t)top);
 }
 
+namespace {
+template <int DT, bool TOP>
+void run_token_logprobs(const LpArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.N * a.S)), rows((unsigned)a.N);
+  if (a.V <= 2048)
+    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, 64>), grid, dim3(64), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, kLpThreads>), grid, dim3(kLpThreads), 0, s, a);
+  if (a.S > 1)
+    hipLaunchKernelGGL((k_token_logprobs_join<DT, TOP>), rows, dim3(kLpThreads), 0, s, a);
+}
+}  // namespace
+
 hipError_t launch_token_logprobs(int dtype, const void *logits, int64_t ld, const Tokens &tokens,
                                  int64_t N, int64_t V, int32_t top, const LpOut &out, void *ws,
                                  hipStream_t s) {
   if (N <= 0) return hipSuccess;
-  const int S = lp_splits(N, V, dtype);
-  LpArgs a{logits, ld, N, V, tokens, top, S, cd(cd(V, S), 8) * 8, nullptr, nullptr, out};
+  int S = lp_splits(N, V, dtype);
+  const int64_t per = cd(cd(V, S), 8) * 8;
+  S = (int)cd(V, per);
+  LpArgs a{logits, ld, N, V, tokens, top, S, per, nullptr, nullptr, out};
   if (S > 1) {
     a.part = (LpPart *)ws;
     a.keys = (uint64_t *)((char *)ws + (size_t)N * S * sizeof(LpPart));
   }
-  const dim3 grid((unsigned)(N * S)), block(kLpThreads), rows((unsigned)N);
-#define KD_LP(DT, TOP)                                                                  \
-  do {                                                                                  \
-    hipLaunchKernelGGL((k_token_logprobs<DT, TOP>), grid, block, 0, s, a);              \
-    if (S > 1)                                                                          \
-      hipLaunchKernelGGL((k_token_logprobs_join<DT, TOP>), rows, block, 0, s, a);       \
-  } while (0)
   if (dtype == 1) {
-    if (top > 0) KD_LP(1, true);
-    else KD_LP(1, false);
+    if (top > 0) run_token_logprobs<1, true>(a, s);
+    else run_token_logprobs<1, false>(a, s);
   } else {
-    if (top > 0) KD_LP(0, true);
-    else KD_LP(0, false);
+    if (top > 0) run_token_logprobs<0, true>(a, s);
+    else run_token_logprobs<0, false>(a, s);
   }
-#undef KD_LP
   return hipGetLastError();
 }
 

@@ -34,32 +34,31 @@ struct LpOut {
 
 // Writes a row's results from its maximum m, S = sum exp(z - m), T = sum exp(z - m)(z - m)
 // and the given token's logit zt.  No finite logit (S = 0): lse = logp = -inf, entropy 0.
-// A NaN or +inf logit (S is NaN): everything NaN.  Returns ln S (double), NaN for a bad row
-// and -inf for an empty one.
-__device__ __forceinline__ double lp_finish(const LpOut &o, long long n, float m, double S,
-                                            double T, long long tok, long long V, float zt) {
+// A NaN or +inf logit (S is NaN): everything NaN.  Returns ln S, NaN for a bad row and -inf
+// for an empty one.  S >= 1 holds the maximum's own term 1: ln S keeps its digits there
+// through ln(1 + x).
+__device__ __forceinline__ float lp_finish(const LpOut &o, long long n, float m, double S,
+                                           double T, long long tok, long long V, float zt) {
   const float nan = __uint_as_float(0x7FC00000u);
   const bool bad = !(S >= 0.0) || !(m < INFINITY), empty = !bad && S == 0.0;
-  double lnS = empty ? -(double)INFINITY : log(S);
+  const float lnS = bad ? nan : empty ? -INFINITY : S < 2.0 ? log1pf((float)(S - 1.0)) : logf((float)S);
   float lp, H, lse, mm = m;
   if (bad) {
     lp = H = lse = mm = nan;
-    lnS = (double)nan;
   } else if (empty) {
     lp = lse = mm = -INFINITY;
     H = 0.f;
   } else {
-    lp = (float)((double)zt - (double)m - lnS);
-    const double h = lnS - T / S;
-    H = h > 0.0 ? (float)h : 0.f;
-    lse = (float)((double)m + lnS);
+    lp = (zt - m) - lnS;
+    H = fmaxf(lnS - (float)(T / S), 0.f);
+    lse = m + lnS;
   }
   if (tok < 0) lp = bad ? nan : 0.f;
   if (tok >= V) lp = nan;
   o.logp[n] = lp;
   o.entropy[n] = H;
   o.lse[n] = lse;
-  if (o.stats) o.stats[n] = make_float2(mm, empty ? 0.f : (float)lnS);
+  if (o.stats) o.stats[n] = make_float2(mm, empty ? 0.f : lnS);
   if (o.status && (bad || tok >= V)) *o.status = o.bad_code;
   return lnS;
 }
