@@ -6,7 +6,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = [os.path.join(PKG, "csrc", f) for f in ("kd_kernels.hip", "kd_api.hip", "kd_topk.hip",
-                                               "kd_logprobs.hip", "kd_head.hip", "kd_clip.hip",
+                                               "kd_logprobs.hip", "kd_head.hip",
+                                               "kd_head_few.hip", "kd_clip.hip",
                                                "kd_ops_api.hip")]
 OUT = os.path.join(PKG, "libkdkl.so")
 

@@ -4,8 +4,10 @@ allocated with torch, and the library's HIP kernels do the work on the current s
 ``stream``).  No call synchronises, so each can be recorded with ``torch.cuda.graph``."""
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -48,6 +50,14 @@ def _on(dev, stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=dev)
             with torch.cuda.stream(stream):
                 yield
+
+
+def _raw_stream(dev):
+    """The handle of torch's current stream on dev (by the short way where torch has it)."""
+    return _CURRENT(dev.index) if _CURRENT else torch.cuda.current_stream(dev).cuda_stream
+
+
+_CURRENT = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _elsewhere(dev, stream) -> bool:
@@ -104,6 +114,7 @@ def _scratch(workspace, need, dev):
     return workspace
 
 
+@functools.lru_cache(maxsize=1024)
 def token_logprobs_workspace_bytes(N: int, V: int, top: int = 0, dtype: int = kd.KD_BF16) -> int:
     """Workspace bytes of ``token_logprobs`` (0 for many rows)."""
     out = ctypes.c_size_t(0)
@@ -114,7 +125,7 @@ def token_logprobs_workspace_bytes(N: int, V: int, top: int = 0, dtype: int = kd
 def _token_logprobs(logits, tokens, top, status, workspace, stats):
     dt = kd._dtype_code(logits)
     dev = logits.device
-    kd._on_device(dev, logits=logits, tokens=tokens, status=status)
+    kd._on_device(dev, tokens=tokens, status=status)
     N, V, ld = _rows(logits, "logits")
     bits = _token_bits(tokens, N)
     workspace = _scratch(workspace, token_logprobs_workspace_bytes(N, V, top, dt), dev)
@@ -128,7 +139,7 @@ def _token_logprobs(logits, tokens, top, status, workspace, stats):
         logits.data_ptr(), dt, ld, tokens.data_ptr(), bits, N, V, top, logp.data_ptr(),
         entropy.data_ptr(), lse.data_ptr(), kd._ptr(st), kd._ptr(idx), kd._ptr(tlp),
         _status_ptr(status), kd._ptr(workspace), 0 if workspace is None else workspace.numel(),
-        torch.cuda.current_stream(dev).cuda_stream))
+        _raw_stream(dev)))
     return (logp, entropy, lse, idx, tlp) if top else (logp, entropy, lse), st
 
 
@@ -185,7 +196,7 @@ def token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp=None, grad_
     kd._check(kd._lib().kd_token_logprobs_bwd(
         logits.data_ptr(), dt, ld, tokens.data_ptr(), bits, N, V, row_stats.data_ptr(),
         entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]), out.data_ptr(), ld_d,
-        torch.cuda.current_stream(dev).cuda_stream))
+        _raw_stream(dev)))
     return out
 
 
@@ -208,6 +219,7 @@ class _TokenLogprobs(torch.autograd.Function):
 
 
 # ---- from hidden states ------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
 def head_logprobs_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
                                   dtype: int = kd.KD_BF16) -> int:
     """Workspace bytes of ``head_logprobs``."""
@@ -251,7 +263,7 @@ def _head_logprobs(h, W, tokens, chunk, status, workspace, stats):
     kd._check(kd._lib().kd_head_logprobs(
         h.data_ptr(), W.data_ptr(), dt, tokens.data_ptr(), bits, N, d, V, chunk, logp.data_ptr(),
         entropy.data_ptr(), lse.data_ptr(), kd._ptr(st), _status_ptr(status),
-        workspace.data_ptr(), workspace.numel(), torch.cuda.current_stream(dev).cuda_stream))
+        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return (logp, entropy, lse), st
 
 
@@ -304,7 +316,7 @@ def head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp=None, grad_ent
         h.data_ptr(), W.data_ptr(), dt, tokens.data_ptr(), bits, N, d, V, chunk,
         row_stats.data_ptr(), entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]),
         kd._ptr(dh), kd._ptr(dW), workspace.data_ptr(), workspace.numel(),
-        torch.cuda.current_stream(dev).cuda_stream))
+        _raw_stream(dev)))
     return dh, dW
 
 
@@ -329,6 +341,9 @@ class _HeadLogprobs(torch.autograd.Function):
 
 
 # ---- gradient norm and clipping -------------------------------------------------------------
+_CODES = {torch.bfloat16: kd.KD_BF16, _F32: kd.KD_F32}
+
+
 def _clip(grads, max_norm, out, workspace, stream):
     if not grads:
         raise ValueError("no tensors")
@@ -340,21 +355,26 @@ def _clip(grads, max_norm, out, workspace, stream):
     n = len(grads)
     if out is not None and len(out) != n:
         raise ValueError(f"{len(out)} outputs for {n} gradients")
-    codes = {torch.bfloat16: kd.KD_BF16, _F32: kd.KD_F32}
+    on = dev.index
     for name, ts in (("grads", grads), ("out", out or ())):
         for i, t in enumerate(ts):
-            if t.device != dev:
+            if t.get_device() != on:
                 kd._on_device(dev, **{f"{name}[{i}]": t})
-            if t.dtype not in codes:
-                raise TypeError(f"{name}[{i}] must be bfloat16 or float32, not {t.dtype}")
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}] must be contiguous")
-            if name == "out" and (t.dtype != grads[i].dtype or t.shape != grads[i].shape):
-                raise ValueError(f"out[{i}] must have the shape and dtype of grads[{i}]")
-    numel = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-    types = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in grads])
-    gp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    op = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    try:
+        types = [_CODES[t.dtype] for t in grads]
+    except KeyError as e:
+        raise TypeError(f"gradients must be bfloat16 or float32, not {e.args[0]}") from None
+    sizes = [t.numel() for t in grads]
+    if out is not None and (sizes != [t.numel() for t in out]
+                            or types != [_CODES.get(t.dtype) for t in out]):
+        raise ValueError("out must have the shapes and dtypes of grads")
+    held = [array.array("q", sizes), array.array("i", types),
+            array.array("Q", [t.data_ptr() for t in grads]),
+            array.array("Q", [t.data_ptr() for t in out or ()])]
+    numel, types, gp, op = (a.buffer_info()[0] for a in held)
+    op = op if out is not None else None
     if workspace is None:
         need = ctypes.c_size_t(0)
         kd._check(kd._lib().kd_clip_grads_workspace_bytes(numel, n, ctypes.byref(need)))
@@ -364,7 +384,7 @@ def _clip(grads, max_norm, out, workspace, stream):
     norm = torch.empty(1, dtype=_F32, device=dev)
     kd._check(kd._lib().kd_clip_grads(gp, op, numel, types, n, max_norm, norm.data_ptr(),
                                       workspace.data_ptr(), workspace.numel(),
-                                      torch.cuda.current_stream(dev).cuda_stream))
+                                      _raw_stream(dev)))
     return norm
 
 

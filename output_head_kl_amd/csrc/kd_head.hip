@@ -87,48 +87,82 @@ struct EpiHeadFwd {
   }
 };
 
-// 64 tokens per workgroup of 16 waves, lane = token: wave w folds the partials w, w + 16,
-// ..., wave 0 the 16 results, in a fixed order.
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(64 * kJoinWaves) void k_head_join(const float2 *part,
-                                                               const float *part_t, int n_lse,
-                                                               long long ld, int rows, int V,
-                                                               const float *zt, Tokens tokens,
-                                                               LpOut out) {
-  __shared__ float sm[kJoinWaves][64];
-  __shared__ double sS[kJoinWaves][64], sT[kJoinWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = blockIdx.x * 64 + lane;
-  float m = -3.4028234663852886e38f;
+// Joins a token's partials, in a fixed order: TOK tokens per workgroup (8, for 64-byte reads
+// where a partial's tokens lie side by side; 1 where a token's partials do), 1024 / TOK
+// threads per token, each up to eight partials at a time; then lanes, then waves.
+constexpr int kJoinThreads = 1024;
+__device__ __forceinline__ void head_join(float &m, double &S, double &T, float m2, double S2,
+                                          double T2) {
+  const float M = __builtin_elementwise_maximum(m, m2);  // NaN stays
+  const float d1 = fmaxf(m - M, kOpLowest), d2 = fmaxf(m2 - M, kOpLowest);
+  const double c1 = (double)fast_exp2(d1 * kLog2e), c2 = (double)fast_exp2(d2 * kLog2e);
+  T = c1 * (T + (double)d1 * S) + c2 * (T2 + (double)d2 * S2);
+  S = c1 * S + c2 * S2;
+  m = M;
+}
+template <int TOK>
+__global__ __launch_bounds__(kJoinThreads) void k_head_join(const float2 *part,
+                                                            const float *part_t, int n_lse,
+                                                            long long si, long long sr, int rows,
+                                                            int V, const float *zt, Tokens tokens,
+                                                            LpOut out) {
+  constexpr int NW = kJoinThreads / 64, SLOTS = kJoinThreads / TOK, U = 8;
+  constexpr float kNone = -3.4028234663852886e38f;
+  __shared__ float sm[NW * TOK];
+  __shared__ double sS[NW * TOK], sT[NW * TOK];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, slot = t / TOK;
+  const int r = blockIdx.x * TOK + t % TOK;
+  float m = kNone;
   double S = 0.0, T = 0.0;
-  auto fold = [&](float m2, double S2, double T2) {
-    const float M = fmaxf(m, m2);
-    const float d1 = fmaxf(m - M, kOpLowest), d2 = fmaxf(m2 - M, kOpLowest);
-    const double c1 = (double)fast_exp2(d1 * kLog2e), c2 = (double)fast_exp2(d2 * kLog2e);
-    T = c1 * (T + (double)d1 * S) + c2 * (T2 + (double)d2 * S2);
-    S = c1 * S + c2 * S2;
-    m = M;
-  };
   if (r < rows)
-    for (int t0 = w; t0 < n_lse; t0 += 4 * kJoinWaves) {
-      float2 q[4];
-      float t2[4];
+    for (int i0 = slot; i0 < n_lse; i0 += U * SLOTS) {
+      float2 q[U];
+      float t2[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int t = t0 + u * kJoinWaves;
-        q[u] = t < n_lse ? part[t * ld + r] : make_float2(-INFINITY, 0.f);
-        t2[u] = t < n_lse ? part_t[t * ld + r] : 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * SLOTS;
+        q[u] = i < n_lse ? part[i * si + r * sr] : make_float2(kNone, 0.f);
+        t2[u] = i < n_lse ? part_t[i * si + r * sr] : 0.f;
       }
+      float M = q[0].x;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (t0 + u * kJoinWaves < n_lse) fold(q[u].x, (double)q[u].y, kOpLn2d * (double)t2[u]);
+      for (int u = 1; u < U; ++u) M = __builtin_elementwise_maximum(M, q[u].x);
+      float s = 0.f, tt = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float d = fmaxf(q[u].x - M, kOpLowest), c = fast_exp2(d * kLog2e);
+        s = fmaf(c, q[u].y, s);
+        tt = fmaf(c, fmaf(t2[u], (float)kOpLn2d, d * q[u].y), tt);
+      }
+      head_join(m, S, T, M, (double)s, (double)tt);
     }
-  sm[w][lane] = m;
-  sS[w][lane] = S;
-  sT[w][lane] = T;
+  auto lanes = [&](int from) {
+#pragma unroll
+    for (int o = TOK; o < 64; o <<= 1) {
+      if (o >= from) break;
+      const float m2 = __shfl_xor(m, o, 64);
+      const double S2 = __shfl_xor(S, o, 64), T2 = __shfl_xor(T, o, 64);
+      head_join(m, S, T, m2, S2, T2);
+    }
+  };
+  lanes(64);
+  if (lane < TOK) {
+    sm[w * TOK + lane] = m;
+    sS[w * TOK + lane] = S;
+    sT[w * TOK + lane] = T;
+  }
   __syncthreads();
-  if (w != 0 || r >= rows) return;
-#pragma unroll 1
-  for (int i = 1; i < kJoinWaves; ++i) fold(sm[i][lane], sS[i][lane], sT[i][lane]);
+  if (w != 0) return;
+  // NW * TOK entries: two per lane, or one for the first of them
+  constexpr int E = NW * TOK;
+  const int e = lane % E;
+  m = sm[e];
+  S = sS[e];
+  T = sT[e];
+  static_assert(E == 128 || E == 16, "entries of the first wave");
+  if (E == 128) head_join(m, S, T, sm[e + E / 2], sS[e + E / 2], sT[e + E / 2]);
+  lanes(E < 64 ? E : 64);
+  if (lane >= TOK || r >= rows) return;
   const long long tok = tokens.at(r);
   lp_finish(out, r, m, S, T, tok, V, tok >= 0 && tok < V ? zt[r] : 0.f);
 }
@@ -316,11 +350,16 @@ hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t ro
   return run_gemm<0, OP_KC, OP_KC>(A, B, G, e, s);
 }
 
-hipError_t launch_head_join(const float2 *part, const float *part_t, int64_t n_lse,
+hipError_t launch_head_join(bool few, const float2 *part, const float *part_t, int64_t n_lse,
                             int64_t ld_part, int64_t rows, int64_t V, const float *zt,
                             const Tokens &tokens, const LpOut &out, hipStream_t s) {
-  hipLaunchKernelGGL(k_head_join, dim3(cdiv(rows, 64)), dim3(64 * kJoinWaves), 0, s, part, part_t,
-                     (int)n_lse, (long long)ld_part, (int)rows, (int)V, zt, tokens, out);
+  if (few)
+    hipLaunchKernelGGL(k_head_join<1>, dim3((unsigned)rows), dim3(kJoinThreads), 0, s, part,
+                       part_t, (int)n_lse, 1LL, (long long)n_lse, (int)rows, (int)V, zt, tokens,
+                       out);
+  else
+    hipLaunchKernelGGL(k_head_join<8>, dim3(cdiv(rows, 8)), dim3(kJoinThreads), 0, s, part, part_t,
+                       (int)n_lse, (long long)ld_part, 1LL, (int)rows, (int)V, zt, tokens, out);
   return hipGetLastError();
 }
 

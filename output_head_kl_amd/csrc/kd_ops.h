@@ -85,7 +85,15 @@ hipError_t launch_token_logprobs_bwd(int dtype, const void *logits, int64_t ld,
 hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
                            int64_t V, const Tokens &tokens, float2 *part, float *part_t,
                            int64_t ld_part, float *zt, hipStream_t s);
-hipError_t launch_head_join(const float2 *part, const float *part_t, int64_t n_lse,
+// The same for at most kHeadFewTokens tokens (kd_head_few.hip): head_few_partials partials of
+// each, one after the other (token r's from r * that on).
+constexpr int64_t kHeadFewTokens = 64;
+int64_t head_few_partials(int64_t N, int64_t V);
+hipError_t launch_head_few(int dtype, const void *W, const void *h, int64_t rows, int64_t d,
+                           int64_t V, const Tokens &tokens, float2 *part, float *part_t,
+                           float *zt, hipStream_t s);
+// Joins the partials (partial i of token r at i * ld + r, or for few at r * n_lse + i).
+hipError_t launch_head_join(bool few, const float2 *part, const float *part_t, int64_t n_lse,
                             int64_t ld_part, int64_t rows, int64_t V, const float *zt,
                             const Tokens &tokens, const LpOut &out, hipStream_t s);
 struct HeadCoef {  // per token of a chunk

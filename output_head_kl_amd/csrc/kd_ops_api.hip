@@ -72,6 +72,7 @@ int check_workspace(const void *workspace, size_t bytes, size_t need) {
 // Forward workspace: the partials of one chunk and its given tokens' logits.
 struct HeadFwd {
   int64_t C, C_alloc, n_lse;
+  bool few;  // few tokens in all: one pass that streams W, whatever the chunk
   size_t off_t, off_zt, total;
 };
 HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
@@ -79,7 +80,9 @@ HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
   L.C = chunk < N ? chunk : (N > 0 ? N : 1);
   L.C_alloc = rup(L.C, 64);
   const int64_t wr = kd::tile_rows(dtype) / 2;
-  L.n_lse = (V + wr - 1) / wr;
+  L.few = N <= kd::kHeadFewTokens;
+  if (L.few) L.C = L.C_alloc = N > 0 ? N : 1;
+  L.n_lse = L.few ? kd::head_few_partials(L.C, V) : (V + wr - 1) / wr;
   L.off_t = (size_t)rup(L.n_lse * L.C_alloc * 8, 256);
   L.off_zt = L.off_t + (size_t)rup(L.n_lse * L.C_alloc * 4, 256);
   L.total = L.off_zt + (size_t)rup(L.C_alloc * 4, 256);
@@ -253,13 +256,15 @@ int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *to
     const int64_t rows = N - c0 < L.C ? N - c0 : L.C;
     const char *h_c = (const char *)h + c0 * d * es;
     const kd::Tokens tok = tokens_at(tokens, token_bits, c0);
-    LAUNCH(kd::KC_FWD_GEMM, kd::launch_head_fwd(dtype, W, h_c, rows, d, V, tok, part, part_t,
-                                                L.C_alloc, zt, stream));
+    LAUNCH(kd::KC_FWD_GEMM,
+           L.few ? kd::launch_head_few(dtype, W, h_c, rows, d, V, tok, part, part_t, zt, stream)
+                 : kd::launch_head_fwd(dtype, W, h_c, rows, d, V, tok, part, part_t, L.C_alloc,
+                                       zt, stream));
     const kd::LpOut out{logp + c0, entropy + c0, row_lse + c0,
                         row_stats ? (float2 *)row_stats + c0 : nullptr, nullptr, nullptr, status,
                         KD_E_INDEX};
-    LAUNCH(kd::KC_LOGPROBS, kd::launch_head_join(part, part_t, L.n_lse, L.C_alloc, rows, V, zt,
-                                                 tok, out, stream));
+    LAUNCH(kd::KC_LOGPROBS, kd::launch_head_join(L.few, part, part_t, L.n_lse, L.C_alloc, rows, V,
+                                                 zt, tok, out, stream));
   }
   return KD_OK;
 }

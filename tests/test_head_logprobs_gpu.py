@@ -61,7 +61,8 @@ def check_grad(name, got, want, dtype):
 
 SIZES = [(1, 8, 1, 2048), (1, 64, 2, 2048), (3, 64, 383, 2048), (5, 72, 385, 2), (17, 264, 3001, 2048),
          (1, 512, 20000, 2048), (64, 256, 5003, 2048), (65, 256, 5003, 64), (300, 136, 2050, 128),
-         (700, 264, 3001, 300)]
+         (700, 264, 3001, 300), (33, 72, 66001, 2048), (20, 264, 70000, 2048), (64, 40, 65537, 64),
+         (16, 136, 66000, 2048)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
