@@ -426,15 +426,15 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
  *
  * kd_head_logprobs_bwd: for upstream gradients gl, ge, gz of logp, entropy and row_lse
  *   ([N] float32; NULL = 0), with dz as in kd_token_logprobs_bwd (rounded to dtype once):
- *   dh = dz W  [N, d] dtype, rounded once;  dW = dz^T h  [V, d] float32, overwritten
- *   (each 16-byte aligned; either may be NULL: not wanted)
+ *   dh = dz W  [N, d] dtype, rounded once;  dW = dz^T h  [V, d] dw_dtype (KD_F32 or dtype),
+ *   overwritten, rounded once (each 16-byte aligned; either may be NULL: not wanted)
  *   row_stats, entropy  from kd_head_logprobs on the same h and W
  *   workspace  kd_head_logprobs_bwd_workspace_bytes(..., 16384, ...) bytes for full speed, at
  *              least (..., 0, ...) bytes; dw_group_tokens as kd_workspace_bytes_group
  * A token >= V makes its row of dh and all of dW NaN.
  *
  * Sizes: N >= 0, d >= 8 with d % 8 == 0, d <= 2^20, 1 <= V <= 2^24, chunk >= 1, min(chunk, N)
- * <= 2^22.  Results do not depend on timing, and on chunk (of the forward) not at all.  No
+ * <= 2^22.  Results do not depend on timing, and on chunk only in the order of float32 sums.  No
  * synchronisation, copy or allocation: every call can be recorded into a HIP graph.
  */
 int kd_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
@@ -444,13 +444,13 @@ int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *to
                      float *logp, float *entropy, float *row_lse, float *row_stats,
                      int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
 int kd_head_logprobs_bwd_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
-                                         int32_t dtype, int64_t dw_group_tokens,
-                                         size_t *bytes_out);
+                                         int32_t dtype, int32_t dw_dtype,
+                                         int64_t dw_group_tokens, size_t *bytes_out);
 int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void *tokens,
                          int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
                          const float *row_stats, const float *entropy, const float *grad_logp,
-                         const float *grad_entropy, const float *grad_lse, void *dh, float *dW,
-                         void *workspace, size_t workspace_bytes, void *stream);
+                         const float *grad_entropy, const float *grad_lse, void *dh, void *dW,
+                         int32_t dw_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * kd_clip_grads -- the global norm of gradients (dh, dW and whatever else a step trains) and

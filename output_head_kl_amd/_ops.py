@@ -29,9 +29,9 @@ def declare(lib) -> None:
             ("kd_head_logprobs_workspace_bytes", [i64, i64, i64, i64, i32, psz]),
             ("kd_head_logprobs", [vp, vp, i32, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                                   vp, sz, vp]),
-            ("kd_head_logprobs_bwd_workspace_bytes", [i64, i64, i64, i64, i32, i64, psz]),
+            ("kd_head_logprobs_bwd_workspace_bytes", [i64, i64, i64, i64, i32, i32, i64, psz]),
             ("kd_head_logprobs_bwd", [vp, vp, i32, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp,
-                                      vp, vp, vp, vp, sz, vp]),
+                                      vp, vp, vp, i32, vp, sz, vp]),
             ("kd_clip_grads_workspace_bytes", [vp, i32, psz]),
             ("kd_clip_grads", [vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, sz, vp])):
         getattr(lib, name).argtypes = args
@@ -220,7 +220,7 @@ class _TokenLogprobs(torch.autograd.Function):
 
 # ---- from hidden states ------------------------------------------------------------------
 @functools.lru_cache(maxsize=1024)
-def head_logprobs_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
+def head_logprobs_workspace_bytes(N: int, d: int, V: int, chunk: int = 4096,
                                   dtype: int = kd.KD_BF16) -> int:
     """Workspace bytes of ``head_logprobs``."""
     out = ctypes.c_size_t(0)
@@ -228,14 +228,15 @@ def head_logprobs_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
     return int(out.value)
 
 
-def head_logprobs_bwd_workspace_bytes(N: int, d: int, V: int, chunk: int = 2048,
-                                      dtype: int = kd.KD_BF16,
+@functools.lru_cache(maxsize=1024)
+def head_logprobs_bwd_workspace_bytes(N: int, d: int, V: int, chunk: int = 4096,
+                                      dtype: int = kd.KD_BF16, dw_dtype: int = kd.KD_F32,
                                       dw_group_tokens: int = 16384) -> int:
     """Workspace bytes of ``head_logprobs_bwd``: for full speed, or for dW groups of at most
-    ``dw_group_tokens`` tokens (0: one chunk, the smallest accepted)."""
+    ``dw_group_tokens`` tokens (0: groups of one chunk)."""
     out = ctypes.c_size_t(0)
-    kd._check(kd._lib().kd_head_logprobs_bwd_workspace_bytes(N, d, V, chunk, dtype,
-                                                             dw_group_tokens, ctypes.byref(out)))
+    kd._check(kd._lib().kd_head_logprobs_bwd_workspace_bytes(
+        N, d, V, chunk, dtype, dw_dtype, dw_group_tokens, ctypes.byref(out)))
     return int(out.value)
 
 
@@ -267,7 +268,7 @@ def _head_logprobs(h, W, tokens, chunk, status, workspace, stats):
     return (logp, entropy, lse), st
 
 
-def head_logprobs(h, W, tokens, chunk: int = 2048, status=None, workspace=None, stream=None):
+def head_logprobs(h, W, tokens, chunk: int = 4096, status=None, workspace=None, stream=None):
     """Log probabilities of given tokens from hidden states, with entropy and logsumexp:
     ``token_logprobs`` of h W^T with no logits in memory.
 
@@ -288,10 +289,10 @@ def head_logprobs(h, W, tokens, chunk: int = 2048, status=None, workspace=None, 
 
 
 def head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp=None, grad_entropy=None,
-                      grad_lse=None, chunk: int = 2048, want_dh: bool = True,
-                      want_dW: bool = True, dw_group_tokens: int = 16384, workspace=None,
-                      stream=None):
-    """(dh [N, d] in h's dtype, dW [V, d] float32) of ``head_logprobs`` for upstream gradients
+                      grad_lse=None, chunk: int = 4096, want_dh: bool = True,
+                      want_dW: bool = True, dW_dtype=torch.float32,
+                      dw_group_tokens: int = 16384, workspace=None, stream=None):
+    """(dh [N, d] in h's dtype, dW [V, d] in ``dW_dtype``, float32 or h's) of ``head_logprobs`` for upstream gradients
     [N] of logp, entropy and lse (None: 0); None for the one that is not wanted.  ``row_stats``
     [N, 2] and ``entropy`` [N] come from the forward; ``workspace`` and ``dw_group_tokens`` as
     in ``fwd_bwd``."""
@@ -300,22 +301,25 @@ def head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp=None, grad_ent
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp, grad_entropy,
-                                     grad_lse, chunk, want_dh, want_dW, dw_group_tokens,
-                                     workspace)
+                                     grad_lse, chunk, want_dh, want_dW, dW_dtype,
+                                     dw_group_tokens, workspace)
     dt, N, d, V, bits = _head(h, W, tokens, row_stats=row_stats, entropy=entropy)
     _float_rows("row_stats", row_stats, (N, 2))
     _float_rows("entropy", entropy, (N,))
     g = [_upstream(n, x, N, dev) for n, x in (("grad_logp", grad_logp),
                                               ("grad_entropy", grad_entropy),
                                               ("grad_lse", grad_lse))]
+    if dW_dtype not in (_F32, W.dtype):
+        raise TypeError(f"dW_dtype must be float32 or {W.dtype}")
+    wt = _CODES[dW_dtype]
     workspace = _scratch(workspace, head_logprobs_bwd_workspace_bytes(
-        N, d, V, chunk, dt, dw_group_tokens) if workspace is None else 0, dev)
+        N, d, V, chunk, dt, wt, dw_group_tokens) if workspace is None else 0, dev)
     dh = torch.empty((N, d), dtype=h.dtype, device=dev) if want_dh else None
-    dW = torch.empty((V, d), dtype=_F32, device=dev) if want_dW else None
+    dW = torch.empty((V, d), dtype=dW_dtype, device=dev) if want_dW else None
     kd._check(kd._lib().kd_head_logprobs_bwd(
         h.data_ptr(), W.data_ptr(), dt, tokens.data_ptr(), bits, N, d, V, chunk,
         row_stats.data_ptr(), entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]),
-        kd._ptr(dh), kd._ptr(dW), workspace.data_ptr(), workspace.numel(),
+        kd._ptr(dh), kd._ptr(dW), wt, workspace.data_ptr(), workspace.numel(),
         _raw_stream(dev)))
     return dh, dW
 
@@ -335,8 +339,7 @@ class _HeadLogprobs(torch.autograd.Function):
         h, W, tokens, st, entropy = ctx.saved_tensors
         dh, dW = head_logprobs_bwd(h, W, tokens, st, entropy, g_logp, g_entropy, g_lse, ctx.chunk,
                                    want_dh=ctx.needs_input_grad[0],
-                                   want_dW=ctx.needs_input_grad[1])
-        # dW is float32; autograd converts it to W's dtype if they differ
+                                   want_dW=ctx.needs_input_grad[1], dW_dtype=W.dtype)
         return dh, dW, None, None, None, None
 
 

@@ -8,6 +8,7 @@
 //  gradient  z again, then dz = p (gz - gl - ge (ln p + H)) + gl [v = t] in one rounding, in
 //            the layouts the dh and dW GEMMs of the loss read.
 #include "kd_gemm.h"
+#include "kd_gemm32.h"
 #include "kd_ops.h"
 
 namespace kd {
@@ -332,22 +333,104 @@ struct EpiHeadDz {
   }
 };
 
+// dh partials of one vocabulary split: tile rows are hidden units j, columns tokens c.
+struct EpiHeadDh {
+  static constexpr bool kPrefetch = false;
+  struct Pre {};
+  float *part;
+  long long split_stride, ld;  // C_alloc * d_pad, d_pad
+  int rows;
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void operator()(f32x16 (&acc)[NRB][NCB], int m0, int n0, int lane,
+                                             int split, char *) const {
+    const int jl = m0 + (lane >> 5) * 4;
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+      const int c = n0 + cb * 32 + (lane & 31);
+      if (c >= rows) continue;
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int j = jl + rb * 32 + g * 8;
+          if (j >= ld) continue;  // d_pad is a multiple of 4
+          *(f32x4 *)(part + split * split_stride + c * ld + j) =
+              f32x4{acc[rb][cb][g * 4], acc[rb][cb][g * 4 + 1], acc[rb][cb][g * 4 + 2],
+                    acc[rb][cb][g * 4 + 3]};
+        }
+    }
+  }
+};
+
+// dW: tile rows are vocabulary entries v, columns hidden units j; the sum over one group of
+// tokens plus, where `old` is given, what earlier groups left there (each element belongs to
+// one lane of one launch).  bf16 is rounded once, here: lanes l and l ^ 1 swap halves of two
+// rows, so that each stores two neighbouring columns of one of them.
+template <int OUT>
+struct EpiHeadDw {
+  static constexpr bool kPrefetch = false;
+  struct Pre {};
+  void *dW;
+  const float *old;
+  int d, V;
+  template <int NRB, int NCB>
+  __device__ __forceinline__ void operator()(f32x16 (&acc)[NRB][NCB], int m0, int n0, int lane,
+                                             int, char *) const {
+    const int vl = m0 + (lane >> 5) * 4;
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const int v = vl + rb * 32 + (i >> 2) * 8 + (i & 3);
+        if (v >= V) continue;
+#pragma unroll
+        for (int cb = 0; cb < NCB; ++cb) {
+          const int j = n0 + cb * 32 + (lane & 31);
+          float x0 = acc[rb][cb][i], x1 = acc[rb][cb][i + 1];
+          if (old && j < d) {
+            x0 += old[(long long)v * d + j];
+            if (v + 1 < V) x1 += old[(long long)(v + 1) * d + j];
+          }
+          if constexpr (OUT == 0) {
+            if (j < d) {
+              ((float *)dW)[(long long)v * d + j] = x0;
+              if (v + 1 < V) ((float *)dW)[(long long)(v + 1) * d + j] = x1;
+            }
+          } else {
+            // d is a multiple of 8: both columns of a pair are inside or neither
+            const float got = __uint_as_float(__builtin_amdgcn_update_dpp(
+                0u, __float_as_uint(odd ? x0 : x1), 0xB1, 0xF, 0xF, true));
+            const unsigned pk = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
+            const int r = v + (odd ? 1 : 0);
+            if (j < d && r < V)
+              *(unsigned *)((unsigned short *)dW + (long long)r * d + (j & ~1)) = pk;
+          }
+        }
+      }
+  }
+};
+
 }  // namespace
+
+int head_part_rows(int dtype, int64_t C, int64_t V) {
+  return dtype == 1 ? kTileA16 / 2 : g32::tile(V, C, 1) / 2;
+}
 
 hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
                            int64_t V, const Tokens &tokens, float2 *part, float *part_t,
-                           int64_t ld_part, float *zt, hipStream_t s) {
+                           int64_t ld_part, int64_t C, float *zt, hipStream_t s) {
   Operand A{W, d, (int)V, (int)d, 256};
   Operand B{h_c, d, (int)rows, (int)d, 256};
-  // token tiles in groups of eight: an XCD's concurrent workgroups then share four vocabulary
-  // tiles and eight token tiles
-  GemmGrid G{cdiv(V, tile_rows(dtype)), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
   if (dtype == 1) {
+    // token tiles in groups of eight: an XCD's concurrent workgroups then share four
+    // vocabulary tiles and eight token tiles
+    GemmGrid G{cdiv(V, kTileA16), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
     EpiHeadFwd<1> e{part, part_t, ld_part, (int)V, (int)rows, tokens, zt};
     return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
   }
   EpiHeadFwd<0> e{part, part_t, ld_part, (int)V, (int)rows, tokens, zt};
-  return run_gemm<0, OP_KC, OP_KC>(A, B, G, e, s);
+  return g32::run<OP_KC, OP_KC>(g32::tile(V, C, 1), V, rows, 1, d, d, A, B, e, s);
 }
 
 hipError_t launch_head_join(bool few, const float2 *part, const float *part_t, int64_t n_lse,
@@ -376,15 +459,88 @@ hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t row
   // vocabulary tiles cover V_pad, so that dz holds zeros from V on
   Operand A{W, d, (int)V, (int)d, 256};
   Operand B{h_c, d, (int)rows, (int)d, 256};
-  GemmGrid G{(int)(V_pad / tile_rows(dtype)), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
   if (dtype == 1) {
+    GemmGrid G{(int)(V_pad / kTileA16), cdiv(rows, kTile), 1, (int)d, (int)d, 0, 8};
     EpiHeadDz<1> e{dz, C_alloc * 256, k.l2, k.a, k.b, k.g, k.tok, (int)V, (int)rows, (int)V_pad,
                    (unsigned short *)dzt, tst};
     return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
   }
   EpiHeadDz<0> e{dz, C_alloc * 256, k.l2, k.a, k.b, k.g, k.tok, (int)V, (int)rows, (int)V_pad,
                  nullptr, 0};
-  return run_gemm<0, OP_KC, OP_KC>(A, B, G, e, s);
+  return g32::run<OP_KC, OP_KC>(g32::tile(V_pad, rows, 1), V_pad, rows, 1, d, d, A, B, e, s);
+}
+
+// The copy costs a read and a write of W, and lets the product read both operands without
+// transposing them in LDS, on a 384-row tile.  201088 x 2880: with the copy 1.49 against 1.07 ms
+// for all gradients of 48 tokens, 12.48 against 13.42 ms for those of 4096.
+bool head_wt(int64_t N) { return N > 1024; }
+
+// The float32 tile of the dh product, which has up to 32 splits to fill the chip.
+static int dh_tile32(int64_t C_alloc, int64_t d) { return g32::tile(d, C_alloc, 32); }
+
+// Enough splits of the vocabulary to fill whole rounds of the workgroups that run at once (one
+// per compute unit in bf16, two in float32); more only where they fill the rounds 5 % better,
+// as each adds a float32 partial of dh.
+void head_dh_splits(int dtype, bool wt, int64_t C_alloc, int64_t d, int64_t V_pad, int *nsplit,
+                    int64_t *k_split) {
+  const int64_t C = C_alloc, t32 = dh_tile32(C_alloc, d);
+  const int64_t tm = dtype == 1 ? (wt ? kTileA16 : kTile) : t32, tn = dtype == 1 ? kTile : t32;
+  const int64_t tiles = ((d + tm - 1) / tm) * ((C + tn - 1) / tn), slots = dtype == 1 ? 256 : 512;
+  int64_t ns = 1;
+  double best = 0.0;
+  for (int64_t c = 1; c <= 32 && c <= V_pad / kTile; ++c) {
+    const int64_t wgs = tiles * c, rounds = (wgs + slots - 1) / slots;
+    const double fill = (double)wgs / (double)(rounds * slots);
+    if ((rounds == 1 && fill > best) || fill > best + 0.05) {
+      best = fill;
+      ns = c;
+    }
+  }
+  *k_split = ((V_pad + ns - 1) / ns + kTile - 1) / kTile * kTile;
+  *nsplit = (int)((V_pad + *k_split - 1) / *k_split);
+}
+
+// D[j][c] = sum_v W[v][j] dz[c][v]
+hipError_t launch_head_dh(int dtype, const void *dz, const void *W, const void *WT, int64_t rows,
+                          int64_t d, int64_t V, int64_t V_pad, int nsplit, int64_t k_split,
+                          float *part, int64_t d_pad, int64_t C_alloc, hipStream_t s) {
+  Operand B{dz, 256, (int)rows, (int)V_pad, C_alloc * 256};
+  EpiHeadDh e{part, C_alloc * d_pad, d_pad, (int)rows};
+  if (dtype == 1) {
+    if (WT) {  // k-contiguous blocks of 256 vocabulary entries
+      GemmGrid G{cdiv(d, kTileA16), cdiv(rows, kTile), nsplit, (int)k_split, (int)V_pad, 0, 0};
+      Operand A{WT, 256, (int)d, (int)V_pad, d * 256};
+      return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
+    }
+    GemmGrid G{cdiv(d, kTile), cdiv(rows, kTile), nsplit, (int)k_split, (int)V_pad, 0, 0};
+    Operand A{W, d, (int)d, (int)V, 256};  // W itself, read transposed through LDS
+    hipLaunchKernelGGL((gemm_pipe_kernel<OP_MC, OP_KC, EpiHeadDh, 2, 2, 64, 4, kTile>),
+                       dim3((unsigned)(G.ntm * G.ntn * G.nsplit)), dim3(512), 0, s, A, B, G, e);
+    return hipGetLastError();
+  }
+  Operand A{W, d, (int)d, (int)V, 256};
+  return g32::run<OP_MC, OP_KC>(dh_tile32(C_alloc, d), d, rows, nsplit, k_split, V_pad, A, B, e, s);
+}
+
+// D[v][j] = sum_c dz[c][v] h[c][j] over k tokens (bf16: dzT and hT in blocks of 256 tokens)
+hipError_t launch_head_dw(int dtype, int out, const void *dz, const void *dzt, const void *h_c,
+                          const void *ht, int64_t k, int64_t d, int64_t V, int64_t V_pad,
+                          int64_t C_alloc, const float *old, void *dW, hipStream_t s) {
+  if (dtype == 1) {
+    GemmGrid G{cdiv(V, kTileA16), cdiv(d, kTile), 1, (int)k, (int)k, 0, 0};
+    Operand A{dzt, 256, (int)V, (int)k, V_pad * 256};
+    Operand B{ht, 256, (int)d, (int)k, d * 256};
+    if (out == 1) {
+      EpiHeadDw<1> e{dW, old, (int)d, (int)V};
+      return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
+    }
+    EpiHeadDw<0> e{dW, old, (int)d, (int)V};
+    return run_gemm<1, OP_KC, OP_KC>(A, B, G, e, s);
+  }
+  Operand A{dz, 256, (int)V_pad, (int)k, C_alloc * 256};
+  Operand B{h_c, d, (int)d, (int)k, 256};
+  EpiHeadDw<0> e{dW, old, (int)d, (int)V};
+  return g32::run<OP_MC, OP_MC>(g32::tile(V, d, 1), V, d, 1, k, k, A, B, e, s);
 }
 
 }  // namespace kd

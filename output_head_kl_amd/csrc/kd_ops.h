@@ -81,10 +81,11 @@ hipError_t launch_token_logprobs_bwd(int dtype, const void *logits, int64_t ld,
                                      void *dlogits, int64_t ld_d, hipStream_t s);
 
 // --- log probabilities from hidden states (kd_head.hip), one token chunk per call ---
-// Partials per (wave row of the vocabulary tile, token): part = (max, S), part_t = T in base 2.
+// Partials per (head_part_rows vocabulary rows, token): part = (max, S), part_t = T in base 2.
+int head_part_rows(int dtype, int64_t C, int64_t V);  // for chunks of C tokens
 hipError_t launch_head_fwd(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
                            int64_t V, const Tokens &tokens, float2 *part, float *part_t,
-                           int64_t ld_part, float *zt, hipStream_t s);
+                           int64_t ld_part, int64_t C, float *zt, hipStream_t s);
 // The same for at most kHeadFewTokens tokens (kd_head_few.hip): head_few_partials partials of
 // each, one after the other (token r's from r * that on).
 constexpr int64_t kHeadFewTokens = 64;
@@ -102,10 +103,26 @@ struct HeadCoef {  // per token of a chunk
 };
 hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows, int64_t V,
                             const HeadCoef &k, hipStream_t s);
-// dz in the layouts of launch_dh_gemm and launch_dw_gemm (dzt null: not wanted).
+// dz as blocks of 256 vocabulary columns (element (c, v) at (v / 256) * C_alloc * 256 + c * 256
+// + v % 256) and, bf16 and wanted, dzT (element (v, c) at (c / 256) * tst + v * 256 + c % 256).
 hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,
                           int64_t V, const HeadCoef &k, void *dz, void *dzt, int64_t tst,
                           int64_t V_pad, int64_t C_alloc, hipStream_t s);
+
+// Whether the dh product of a call with N tokens reads a k-contiguous copy of W (bf16), and
+// into how many vocabulary splits (of k_split entries, a multiple of 256) it goes.
+bool head_wt(int64_t N);
+void head_dh_splits(int dtype, bool wt, int64_t C_alloc, int64_t d, int64_t V_pad, int *nsplit,
+                    int64_t *k_split);
+// dh partials [nsplit][C_alloc][d_pad]; bf16 reads W through WT (launch_transpose_w), or itself
+// where WT is null.
+hipError_t launch_head_dh(int dtype, const void *dz, const void *W, const void *WT, int64_t rows,
+                          int64_t d, int64_t V, int64_t V_pad, int nsplit, int64_t k_split,
+                          float *part, int64_t d_pad, int64_t C_alloc, hipStream_t s);
+// dW of type out = dz^T h over k tokens, plus old (float32, may be dW itself) where given.
+hipError_t launch_head_dw(int dtype, int out, const void *dz, const void *dzt, const void *h_c,
+                          const void *ht, int64_t k, int64_t d, int64_t V, int64_t V_pad,
+                          int64_t C_alloc, const float *old, void *dW, hipStream_t s);
 
 // --- gradient norm and clipping (kd_clip.hip) ---
 // Float64 partials of the squares' sum (one per chunk of a tensor).

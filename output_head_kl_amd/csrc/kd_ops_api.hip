@@ -79,7 +79,7 @@ HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
   HeadFwd L;
   L.C = chunk < N ? chunk : (N > 0 ? N : 1);
   L.C_alloc = rup(L.C, 64);
-  const int64_t wr = kd::tile_rows(dtype) / 2;
+  const int64_t wr = kd::head_part_rows(dtype, L.C, V);
   L.few = N <= kd::kHeadFewTokens;
   if (L.few) L.C = L.C_alloc = N > 0 ? N : 1;
   L.n_lse = L.few ? kd::head_few_partials(L.C, V) : (V + wr - 1) / wr;
@@ -87,6 +87,51 @@ HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
   L.off_zt = L.off_t + (size_t)rup(L.n_lse * L.C_alloc * 4, 256);
   L.total = L.off_zt + (size_t)rup(L.C_alloc * 4, 256);
   return L;
+}
+
+// Backward workspace.  The dW sum runs over groups of chunks; with more than one group and
+// dW not float32 the sum of the earlier ones is kept in float32 here.
+struct HeadBwd {
+  int64_t C, C_alloc, V_pad, d_pad, nchunks, group, k_split;
+  int nsplit;
+  bool wt;  // bf16: the dh product reads a k-contiguous copy of W
+  size_t off_coef, off_dz, off_dhpart, off_wt, off_dzt, off_ht, off_acc, total;
+};
+HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, int dtype, int dw_dtype,
+                        bool want_dh, bool want_dw, int64_t group) {
+  HeadBwd L;
+  const bool bf16 = dtype == KD_BF16;
+  const int64_t es = bf16 ? 2 : 4, n = N > 0 ? N : 1;
+  L.C = chunk < n ? chunk : n;
+  L.C_alloc = rup(L.C, kd::kTile);
+  L.V_pad = rup(V, bf16 ? 3 * kd::kTile : kd::kTile);
+  L.d_pad = rup(d, kd::kTile);
+  L.nchunks = (n + L.C - 1) / L.C;
+  L.group = !bf16 || group < 1 ? 1 : group < L.nchunks ? group : L.nchunks;
+  L.wt = bf16 && kd::head_wt(N);
+  kd::head_dh_splits(dtype, L.wt, L.C_alloc, d, L.V_pad, &L.nsplit, &L.k_split);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t o = off;
+    off += (size_t)rup(bytes, 256);
+    return o;
+  };
+  L.off_coef = take(5 * L.C_alloc * 4);
+  L.off_dz = take(L.C_alloc * L.V_pad * es);
+  L.off_dhpart = take(want_dh ? L.nsplit * L.C_alloc * L.d_pad * 4 : 0);
+  L.off_wt = take(want_dh && L.wt ? L.V_pad * d * 2 : 0);
+  L.off_dzt = take(want_dw && bf16 ? L.group * L.C_alloc * L.V_pad * 2 : 0);
+  L.off_ht = take(want_dw && bf16 ? L.group * L.C_alloc * d * 2 : 0);
+  L.off_acc = take(want_dw && dw_dtype != KD_F32 && L.group < L.nchunks ? V * d * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+// Chunks per group of at most `tokens` tokens (at most kDwGroupTokens, as in the loss).
+int64_t group_chunks(int64_t tokens, int64_t N, int64_t chunk) {
+  const int64_t n = N > 0 ? N : 1, C = rup(chunk < n ? chunk : n, kd::kTile);
+  const int64_t t = tokens < kd::kDwGroupTokens ? tokens : kd::kDwGroupTokens;
+  return t / C < 1 ? 1 : t / C;
 }
 
 kd::Tokens tokens_at(const void *tokens, int32_t token_bits, int64_t c0) {
@@ -259,7 +304,7 @@ int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *to
     LAUNCH(kd::KC_FWD_GEMM,
            L.few ? kd::launch_head_few(dtype, W, h_c, rows, d, V, tok, part, part_t, zt, stream)
                  : kd::launch_head_fwd(dtype, W, h_c, rows, d, V, tok, part, part_t, L.C_alloc,
-                                       zt, stream));
+                                       L.C, zt, stream));
     const kd::LpOut out{logp + c0, entropy + c0, row_lse + c0,
                         row_stats ? (float2 *)row_stats + c0 : nullptr, nullptr, nullptr, status,
                         KD_E_INDEX};
@@ -270,57 +315,65 @@ int kd_head_logprobs(const void *h, const void *W, int32_t dtype, const void *to
 }
 
 int kd_head_logprobs_bwd_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
-                                         int32_t dtype, int64_t dw_group_tokens,
-                                         size_t *bytes_out) {
+                                         int32_t dtype, int32_t dw_dtype,
+                                         int64_t dw_group_tokens, size_t *bytes_out) {
   set_error(KD_OK, nullptr);
   if (!bytes_out) return set_error(KD_E_ARG, "bytes_out is NULL");
   int rc = check_head(nullptr, nullptr, dtype, nullptr, 0, N, d, V, chunk, false);
   if (rc != KD_OK) return rc;
+  if (dw_dtype != KD_F32 && dw_dtype != dtype)
+    return set_error(KD_E_ARG, "dw_dtype is KD_F32 or dtype");
   if (dw_group_tokens < 0) return set_error(KD_E_ARG, "dw_group_tokens is negative");
-  if (dw_group_tokens > kd::kDwGroupTokens) dw_group_tokens = kd::kDwGroupTokens;
-  kd::Layout L;
-  kd::make_layout(N, d, V, 1, chunk, dtype, dw_group_tokens, &L);
-  *bytes_out = L.total;
+  *bytes_out = head_bwd_layout(N, d, V, chunk, dtype, dw_dtype, true, true,
+                               group_chunks(dw_group_tokens, N, chunk)).total;
   return KD_OK;
 }
 
 int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void *tokens,
                          int32_t token_bits, int64_t N, int64_t d, int64_t V, int64_t chunk,
                          const float *row_stats, const float *entropy, const float *grad_logp,
-                         const float *grad_entropy, const float *grad_lse, void *dh, float *dW,
-                         void *workspace, size_t workspace_bytes, void *stream_v) {
+                         const float *grad_entropy, const float *grad_lse, void *dh, void *dW,
+                         int32_t dw_dtype, void *workspace, size_t workspace_bytes,
+                         void *stream_v) {
   set_error(KD_OK, nullptr);
   int rc = check_head(h, W, dtype, tokens, token_bits, N, d, V, chunk, true);
   if (rc != KD_OK) return rc;
   if (!dh && !dW) return set_error(KD_E_ARG, "neither dh nor dW is wanted");
+  if (dw_dtype != KD_F32 && dw_dtype != dtype)
+    return set_error(KD_E_ARG, "dw_dtype is KD_F32 or dtype");
   if (N > 0 && (!row_stats || !entropy))
     return set_error(KD_E_ARG, "row_stats and entropy are required when N > 0");
   if (mis(row_stats, 8)) return set_error(KD_E_ARG, "row_stats must be 8-byte aligned");
   if (mis(entropy, 4) || mis(grad_logp, 4) || mis(grad_entropy, 4) || mis(grad_lse, 4))
     return set_error(KD_E_ARG, "float arguments must be 4-byte aligned");
   if (mis(dh, 16) || mis(dW, 16)) return set_error(KD_E_ARG, "dh and dW must be 16-byte aligned");
-  // the dW group is the largest (up to kDwGroupTokens tokens) whose copies fit
-  kd::Layout L;
-  kd::make_layout(N, d, V, 1, chunk, dtype, kd::kDwGroupTokens, &L);
-  while (workspace_bytes < L.total && L.dw_group > 1)
-    kd::make_layout(N, d, V, 1, chunk, dtype, (int64_t)(L.dw_group - 1) * L.C_alloc, &L);
+  // the dW group is the largest (up to kDwGroupTokens tokens) that fits
+  HeadBwd L;
+  for (int64_t g = group_chunks(kd::kDwGroupTokens, N, chunk); g >= 1; --g) {
+    L = head_bwd_layout(N, d, V, chunk, dtype, dw_dtype, dh != nullptr, dW != nullptr, g);
+    if (workspace_bytes >= L.total) break;
+  }
   rc = check_workspace(workspace, workspace_bytes, L.total);
   if (rc != KD_OK) return rc;
   hipStream_t stream = (hipStream_t)stream_v;
+  const bool bf16 = dtype == KD_BF16;
+  const int64_t es = bf16 ? 2 : 4, tst_dz = L.V_pad * 256, tst_h = d * 256;
   if (N == 0) {
-    if (dW) LAUNCH(kd::KC_MISC, kd::launch_fill_zero(dW, (size_t)V * d * 4, stream));
+    if (dW)
+      LAUNCH(kd::KC_MISC,
+             kd::launch_fill_zero(dW, (size_t)V * d * (dw_dtype == KD_F32 ? 4 : 2), stream));
     return KD_OK;
   }
   char *ws = (char *)workspace;
-  const kd::HeadCoef k{(float *)(ws + L.off_lse), (float *)(ws + L.off_sM), (float *)(ws + L.off_s),
-                       (float *)(ws + L.off_zg), (int *)(ws + L.off_idxloc)};
-  void *dz = ws + L.off_dz, *WT = ws + L.off_wt;
-  const bool bf16 = dtype == KD_BF16, copies = bf16 && dW;  // token-contiguous dW operands
+  float *coef = (float *)(ws + L.off_coef);
+  const kd::HeadCoef k{coef, coef + L.C_alloc, coef + 2 * L.C_alloc, coef + 3 * L.C_alloc,
+                       (int *)(coef + 4 * L.C_alloc)};
+  void *dz = ws + L.off_dz, *WT = L.wt ? ws + L.off_wt : nullptr;
   float *dhpart = (float *)(ws + L.off_dhpart);
-  const int64_t es = bf16 ? 2 : 4, tst_dz = L.V_pad * 256, tst_h = d * 256;
-  if (dh && bf16)
+  if (dh && WT)
     LAUNCH(kd::KC_TRANSPOSE, kd::launch_transpose_w(W, V, d, L.V_pad, WT, stream));
-  int chunk_i = 0, dw_launches = 0;
+  int64_t chunk_i = 0;
+  float *sum = nullptr;  // the earlier groups' sum
   for (int64_t c0 = 0; c0 < N; c0 += L.C, ++chunk_i) {
     const int64_t rows = N - c0 < L.C ? N - c0 : L.C;
     const char *h_c = (const char *)h + c0 * d * es;
@@ -330,12 +383,12 @@ int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void
                        grad_lse ? grad_lse + c0 : nullptr};
     LAUNCH(kd::KC_LOGPROBS_BWD,
            kd::launch_head_coef(tokens_at(tokens, token_bits, c0), g, rows, V, k, stream));
-    const int slot = chunk_i % L.dw_group;
-    void *dzt_c = copies ? ws + L.off_dzt + (size_t)slot * L.C_alloc * L.V_pad * 2 : nullptr;
+    const int64_t slot = chunk_i % L.group;
+    void *dzt_c = bf16 && dW ? ws + L.off_dzt + (size_t)slot * L.C_alloc * L.V_pad * 2 : nullptr;
     LAUNCH(kd::KC_BWD_GEMM, kd::launch_head_dz(dtype, W, h_c, rows, d, V, k, dz, dzt_c, tst_dz,
                                                L.V_pad, L.C_alloc, stream));
     if (dh) {
-      LAUNCH(kd::KC_DH_GEMM, kd::launch_dh_gemm(dtype, dz, W, WT, rows, d, V, L.V_pad, L.nsplit,
+      LAUNCH(kd::KC_DH_GEMM, kd::launch_head_dh(dtype, dz, W, WT, rows, d, V, L.V_pad, L.nsplit,
                                                 L.k_split, dhpart, L.d_pad, L.C_alloc, stream));
       LAUNCH(kd::KC_DH_REDUCE, kd::launch_dh_reduce(dtype, dhpart, L.nsplit, L.C_alloc, L.d_pad,
                                                     rows, d, (char *)dh + c0 * d * es, stream));
@@ -346,13 +399,16 @@ int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void
       LAUNCH(kd::KC_TRANSPOSE,
              kd::launch_transpose_h(h_c, rows, d, L.C_alloc,
                                     (char *)ht + (size_t)slot * L.C_alloc * d * 2, tst_h, stream));
-    if (slot == L.dw_group - 1 || c0 + rows >= N) {
+    const bool last = c0 + rows >= N;
+    if (slot == L.group - 1 || last) {
       // every earlier chunk of the group is whole: its columns past C are zero
-      const int64_t kk = (int64_t)slot * L.C_alloc + rows;
+      const int64_t kk = slot * L.C_alloc + rows;
+      const int out = last ? dw_dtype : (int)KD_F32;
+      void *to = last || dw_dtype == KD_F32 ? dW : (void *)(ws + L.off_acc);
       LAUNCH(kd::KC_DW_GEMM,
-             kd::launch_dw_gemm(dtype, dz, bf16 ? ws + L.off_dzt : nullptr, h_c, ht, kk, d, V,
-                                L.V_pad, L.C_alloc, dW, dw_launches > 0, stream));
-      ++dw_launches;
+             kd::launch_head_dw(dtype, out, dz, bf16 ? ws + L.off_dzt : nullptr, h_c, ht, kk, d, V,
+                                L.V_pad, L.C_alloc, sum, to, stream));
+      sum = (float *)to;
     }
   }
   return KD_OK;

@@ -17,9 +17,9 @@ def fwd(h=A, W=A, dtype=1, tokens=A, bits=64, N=4, d=64, V=64, chunk=2, logp=A, 
 
 
 def bwd(h=A, W=A, dtype=1, tokens=A, bits=64, N=4, d=64, V=64, chunk=2, stats=A, entropy=A, gl=A,
-        ge=A, gz=A, dh=A, dW=A, ws=A, ws_bytes=1 << 40):
+        ge=A, gz=A, dh=A, dW=A, wt=0, ws=A, ws_bytes=1 << 40):
     return kd._lib().kd_head_logprobs_bwd(h, W, dtype, tokens, bits, N, d, V, chunk, stats,
-                                          entropy, gl, ge, gz, dh, dW, ws, ws_bytes, None)
+                                          entropy, gl, ge, gz, dh, dW, wt, ws, ws_bytes, None)
 
 
 COMMON = [
@@ -42,7 +42,7 @@ def test_forward_refusals(change, code):
 @pytest.mark.parametrize("change,code", COMMON + [
     (dict(dh=None, dW=None), E_ARG), (dict(stats=None), E_ARG), (dict(entropy=None), E_ARG),
     (dict(dh=A + 8), E_ARG), (dict(dW=A + 8), E_ARG), (dict(gl=A + 2), E_ARG),
-    (dict(stats=A + 4), E_ARG)])
+    (dict(stats=A + 4), E_ARG), (dict(wt=2), E_ARG), (dict(dtype=0, wt=1), E_ARG)])
 def test_backward_refusals(change, code):
     assert bwd(**change) == code and kd._lib().kd_last_error() != b""
 
@@ -61,7 +61,7 @@ def test_workspace_bytes():
     lib = kd._lib()
     assert lib.kd_head_logprobs_workspace_bytes(1, 12, 5, 1, 1, ctypes.byref(out)) == E_UNSUPPORTED
     assert lib.kd_head_logprobs_workspace_bytes(1, 16, 5, 1, 1, None) == E_ARG
-    assert lib.kd_head_logprobs_bwd_workspace_bytes(1, 16, 5, 1, 1, -1, ctypes.byref(out)) == E_ARG
+    assert lib.kd_head_logprobs_bwd_workspace_bytes(1, 16, 5, 1, 1, 0, -1, ctypes.byref(out)) == E_ARG
 
 
 @pytest.mark.parametrize("device", ["cpu", "meta"])
