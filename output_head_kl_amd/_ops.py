@@ -14,6 +14,7 @@ import torch
 import output_head_kl_amd as kd
 
 _F32 = torch.float32
+_CODES = {torch.bfloat16: kd.KD_BF16, _F32: kd.KD_F32}
 
 
 def declare(lib) -> None:
@@ -122,10 +123,24 @@ def token_logprobs_workspace_bytes(N: int, V: int, top: int = 0, dtype: int = kd
     return int(out.value)
 
 
+def _code(t, name):
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}") from None
+
+
+def _same_device(dev, **tensors):
+    """kd._on_device without its message unless there is one to give."""
+    for t in tensors.values():
+        if t is not None and t.device != dev:
+            kd._on_device(dev, **tensors)
+
+
 def _token_logprobs(logits, tokens, top, status, workspace, stats):
-    dt = kd._dtype_code(logits)
+    dt = _code(logits, "logits")
     dev = logits.device
-    kd._on_device(dev, tokens=tokens, status=status)
+    _same_device(dev, tokens=tokens, status=status)
     N, V, ld = _rows(logits, "logits")
     bits = _token_bits(tokens, N)
     workspace = _scratch(workspace, token_logprobs_workspace_bytes(N, V, top, dt), dev)
@@ -180,7 +195,7 @@ def token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp=None, grad_
         with _on(dev, stream):
             return token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp,
                                       grad_entropy, grad_lse, out)
-    dt = kd._dtype_code(logits)
+    dt = _code(logits, "logits")
     N, V, ld = _rows(logits, "logits")
     bits = _token_bits(tokens, N)
     _float_rows("row_stats", row_stats, (N, 2))
@@ -200,22 +215,49 @@ def token_logprobs_bwd(logits, tokens, row_stats, entropy, grad_logp=None, grad_
     return out
 
 
+def _f32(g):
+    """An upstream gradient that autograd has checked, as the library reads it."""
+    if g is None or (g.dtype is _F32 and g.is_contiguous()):
+        return g
+    return g.to(_F32).contiguous()
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top, status, workspace):
         ctx.set_materialize_grads(False)
         outs, st = _token_logprobs(logits, tokens, top, status, workspace, True)
-        ctx.save_for_backward(logits, tokens, st, outs[1])
+        ctx.save_for_backward(logits, tokens, outs[1])
+        ctx.row_stats = st
         if top:
             ctx.mark_non_differentiable(*outs[3:])
         return outs
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g_logp, g_entropy, g_lse, *_):
-        logits, tokens, st, entropy = ctx.saved_tensors
-        grad = token_logprobs_bwd(logits, tokens, st, entropy, g_logp, g_entropy, g_lse)
-        return grad, None, None, None, None
+    def backward(ctx, *grads):
+        # the arguments were checked by the forward, so only what autograd gives is looked at;
+        # with create_graph the slower wrapper marks the result as differentiable once
+        return (_token_backward_once if torch.is_grad_enabled() else _token_backward)(ctx, *grads)
+
+
+def _token_backward(ctx, g_logp, g_entropy, g_lse, *_):
+    logits, tokens, entropy = ctx.saved_tensors
+    dev = logits.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _token_backward(ctx, g_logp, g_entropy, g_lse)
+    N, V = logits.shape
+    g = _f32(g_logp), _f32(g_entropy), _f32(g_lse)
+    out = torch.empty((N, V), dtype=logits.dtype, device=dev)
+    kd._check(kd._lib().kd_token_logprobs_bwd(
+        logits.data_ptr(), _CODES[logits.dtype], logits.stride(0) if N > 1 else V,
+        tokens.data_ptr(), 64 if tokens.dtype is torch.int64 else 32, N, V,
+        ctx.row_stats.data_ptr(), entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]),
+        kd._ptr(g[2]), out.data_ptr(), V, _raw_stream(dev)))
+    return out, None, None, None, None
+
+
+_token_backward_once = torch.autograd.function.once_differentiable(_token_backward)
 
 
 # ---- from hidden states ------------------------------------------------------------------
@@ -241,8 +283,8 @@ def head_logprobs_bwd_workspace_bytes(N: int, d: int, V: int, chunk: int = 4096,
 
 
 def _head(h, W, tokens, **more):
-    kd._on_device(h.device, h=h, W=W, tokens=tokens, **more)
-    dt = kd._dtype_code(h)
+    _same_device(h.device, W=W, tokens=tokens, **more)
+    dt = _code(h, "h")
     if W.dtype != h.dtype:
         raise TypeError("h and W must have the same dtype")
     if h.dim() != 2 or W.dim() != 2 or W.shape[1] != h.shape[1]:
@@ -329,24 +371,42 @@ class _HeadLogprobs(torch.autograd.Function):
     def forward(ctx, h, W, tokens, chunk, status, workspace):
         ctx.set_materialize_grads(False)
         outs, st = _head_logprobs(h, W, tokens, chunk, status, workspace, True)
-        ctx.save_for_backward(h, W, tokens, st, outs[1])
+        ctx.save_for_backward(h, W, tokens, outs[1])
+        ctx.row_stats = st
         ctx.chunk = chunk
         return outs
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, g_logp, g_entropy, g_lse):
-        h, W, tokens, st, entropy = ctx.saved_tensors
-        dh, dW = head_logprobs_bwd(h, W, tokens, st, entropy, g_logp, g_entropy, g_lse, ctx.chunk,
-                                   want_dh=ctx.needs_input_grad[0],
-                                   want_dW=ctx.needs_input_grad[1], dW_dtype=W.dtype)
-        return dh, dW, None, None, None, None
+    def backward(ctx, *grads):
+        return (_head_backward_once if torch.is_grad_enabled() else _head_backward)(ctx, *grads)
+
+
+def _head_backward(ctx, g_logp, g_entropy, g_lse):
+    h, W, tokens, entropy = ctx.saved_tensors
+    dev = h.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _head_backward(ctx, g_logp, g_entropy, g_lse)
+    N, d = h.shape
+    V = W.shape[0]
+    code = _CODES[h.dtype]
+    g = _f32(g_logp), _f32(g_entropy), _f32(g_lse)
+    dh = torch.empty((N, d), dtype=h.dtype, device=dev) if ctx.needs_input_grad[0] else None
+    dW = torch.empty((V, d), dtype=W.dtype, device=dev) if ctx.needs_input_grad[1] else None
+    need = head_logprobs_bwd_workspace_bytes(N, d, V, ctx.chunk, code, code)
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    kd._check(kd._lib().kd_head_logprobs_bwd(
+        h.data_ptr(), W.data_ptr(), code, tokens.data_ptr(),
+        64 if tokens.dtype is torch.int64 else 32, N, d, V, ctx.chunk, ctx.row_stats.data_ptr(),
+        entropy.data_ptr(), kd._ptr(g[0]), kd._ptr(g[1]), kd._ptr(g[2]), kd._ptr(dh),
+        kd._ptr(dW), code, workspace.data_ptr(), need, _raw_stream(dev)))
+    return dh, dW, None, None, None, None
+
+
+_head_backward_once = torch.autograd.function.once_differentiable(_head_backward)
 
 
 # ---- gradient norm and clipping -------------------------------------------------------------
-_CODES = {torch.bfloat16: kd.KD_BF16, _F32: kd.KD_F32}
-
-
 def _clip(grads, max_norm, out, workspace, stream):
     if not grads:
         raise ValueError("no tensors")
