@@ -14,14 +14,8 @@
 namespace kd {
 namespace {
 
-#ifndef LP_NT
-#define LP_NT 256
-#endif
-#ifndef LP_U
-#define LP_U 4
-#endif
-constexpr int kLpThreads = LP_NT;
-constexpr int kLpSlots = LP_U;  // 16-byte loads in flight per thread and step
+constexpr int kLpThreads = 256;
+constexpr int kLpSlots = 4;  // 16-byte loads in flight per thread and step
 
 template <int DT> struct LpT;
 template <> struct LpT<1> { static constexpr int EPL = 8, ES = 2; };
@@ -126,6 +120,23 @@ __device__ __forceinline__ K wave_sort(K v, int lane) {
   v = sort_down<16>(v, lane, (lane & 32) == 0);
   return sort_down<32>(v, lane, true);
 }
+// A value that at least n <= 64 of the wave's 64 U maxima reach: their n-th largest, found bit by
+// bit from the top by counting and cut off after 16 bits (all there are in bf16).
+template <int U>
+__device__ __forceinline__ float wave_nth(const float (&x)[U], int n) {
+  unsigned key[U], t = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) key[u] = val_key(x[u]);
+#pragma unroll 1
+  for (unsigned bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+    int c = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) c += __popcll(__builtin_amdgcn_ballot_w64(key[u] >= (t | bit)));
+    if (c >= n) t |= bit;
+    if (c == n) break;
+  }
+  return t > val_key(-INFINITY) ? key_val(t) : -INFINITY;
+}
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int l) {
   const unsigned lo = __shfl((unsigned)v, l, 64), hi = __shfl((unsigned)(v >> 32), l, 64);
   return ((uint64_t)hi << 32) | lo;
@@ -151,19 +162,25 @@ __device__ __forceinline__ uint64_t wave_best(const volatile uint64_t *keys, int
 // which is a few dozen of a row's thousands.
 // An element is a candidate if it is above the threshold, or equal to it with an index below
 // `tie`.  Every threshold is a value that at least `top` elements of the row reach: the top-th
-// largest of the 64 lanes' maxima, another wave's threshold (ties are let in), or, where the
-// buffer was cut back to its largest, the top-th of those (ties with a larger index are not).
+// largest of the running maxima of 64 lanes x 4 slots, another wave's threshold (ties are let
+// in), or, where the buffer was cut back to its largest, the top-th of those (ties with a larger
+// index are not).
+// Up to kLpFew alternatives take the threshold from the 64 lanes' maxima, one sort of them
+// (200000 float32 logits, 5: 11 us against 15); more from the maxima of lanes and slots, which
+// are not as close to the top-th largest of a lane (60000 logits, 50: 20 us against 23).
+constexpr int kLpFew = 24;
 constexpr int kLpBuf = 256;   // keys of candidates per wave
 constexpr int kLpNotes = 384; // noted groups per wave: room for a whole step is kept
 struct WaveTop {
   float thr;
   unsigned tie;
-  int cnt, notes, top, lane;
+  int cnt, notes, masked, top, lane;
   volatile uint64_t *buf;
   volatile unsigned *note;
-  __device__ __forceinline__ void init(int top_, int lane_, volatile uint64_t *b,
+  __device__ __forceinline__ void init(int top_, int epl, int lane_, volatile uint64_t *b,
                                        volatile unsigned *n) {
     thr = -INFINITY;
+    masked = (top_ + epl - 1) / epl;
     tie = ~0u;
     cnt = notes = 0;
     top = top_;
@@ -200,42 +217,54 @@ struct WaveTop {
   }
   // Notes the group at index idx whose maximum is mx, if it can hold a candidate.
   __device__ __forceinline__ void look(float mx, unsigned idx) {
-    const bool in = above(mx, idx);
-    const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+    bool in = above(mx, idx);
+    uint64_t mask = __builtin_amdgcn_ballot_w64(in);
     if (mask == 0) return;
+    // masked groups (all -inf, in index order): the first `top` elements' worth is enough
+    const uint64_t none = __builtin_amdgcn_ballot_w64(in && mx == -INFINITY);
+    if (none) {
+      in = in && (mx > -INFINITY || prefix(none) < masked);
+      masked -= min(masked, (int)__popcll(none));
+      mask = __builtin_amdgcn_ballot_w64(in);
+    }
     if (in) note[notes + prefix(mask)] = idx;
     notes += __popcll(mask);
   }
   // Reads the noted groups (at: from index to address; end: the range's) and keeps their
-  // candidates.
+  // candidates, `most` of them at the end.
   template <int DT, class At>
-  __device__ __forceinline__ void drain(unsigned end, At at) {
+  __device__ __forceinline__ void drain(unsigned end, int most, At at) {
     constexpr int EPL = LpT<DT>::EPL;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    for (int i = 0;; i += 64) {
-      const bool has = i + lane < notes, done = i >= notes;
-      const unsigned e = has ? note[i + lane] : 0u;
-      // a group at the end is read from the last whole group's place: skip what precedes it
-      const unsigned from = has && e + EPL <= end ? e : end - EPL;
-      u4 r = load16(at(from));
+    bool has = false;
+    unsigned e = 0, from = 0;
+    u4 r = {0u, 0u, 0u, 0u};
 #pragma unroll 1
-      for (int j = 0; j < EPL; ++j) {
-        // room for 64 more; at the end no more than 64
-        if (cnt > (done ? 64 : kLpBuf - 64)) cut();
-        if (done) break;
-        const float x = __uint_as_float(DT == 0 ? r[0] : r[0] << 16);
-        const bool in = has && from + j >= e && above(x, from + j);
-        const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
-        if (in) buf[cnt + prefix(mask)] = sel_key(x, from + j);
-        cnt += __popcll(mask);
-        if (DT == 0) {
-          r = u4{r[1], r[2], r[3], 0u};
-        } else {
-          r = u4{(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
-                 (r[2] >> 16) | (r[3] << 16), r[3] >> 16};
-        }
+    for (int i = 0, j = EPL;; ++j) {
+      const bool done = j == EPL && i >= notes;
+      if (j == EPL && !done) {  // the next groups, one per lane
+        has = i + lane < notes;
+        e = has ? note[i + lane] : 0u;
+        // a group at the end is read from the last whole group's place: skip what precedes it
+        from = has && e + EPL <= end ? e : end - EPL;
+        r = load16(at(from));
+        i += 64;
+        j = 0;
       }
+      // room for 64 more (the cut is long, and so in one place)
+      if (cnt > (done ? most : kLpBuf - 64)) cut();
       if (done) break;
+      const float x = __uint_as_float(DT == 0 ? r[0] : r[0] << 16);
+      const bool in = has && from + j >= e && above(x, from + j);
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+      if (in) buf[cnt + prefix(mask)] = sel_key(x, from + j);
+      cnt += __popcll(mask);
+      if (DT == 0) {
+        r = u4{r[1], r[2], r[3], 0u};
+      } else {
+        r = u4{(r[0] >> 16) | (r[1] << 16), (r[1] >> 16) | (r[2] << 16),
+               (r[2] >> 16) | (r[3] << 16), r[3] >> 16};
+      }
     }
     notes = 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -282,15 +311,28 @@ struct LpArgs {
   LpOut out;
 };
 
-// The row's alternatives from the sorted list (lane k holds the k-th).
-__device__ __forceinline__ void write_top(const LpOut &o, long long row, int top, int lane,
+// The row's r-th alternative (key 0: there is none, in a bad row).
+__device__ __forceinline__ void write_top(const LpOut &o, long long row, int top, int r,
                                           uint64_t key, float m, float lnS) {
-  if (lane >= top) return;
   const float nan = __uint_as_float(0x7FC00000u);
   const bool bad = lnS != lnS, empty = lnS == -INFINITY;
   const float x = key_val((unsigned)(key >> 32));
-  o.top_idx[row * top + lane] = bad ? -1 : (int32_t)~(unsigned)key;
-  o.top_logp[row * top + lane] = bad ? nan : empty ? -INFINITY : (x - m) - lnS;
+  o.top_idx[row * top + r] = bad ? -1 : (int32_t)~(unsigned)key;
+  o.top_logp[row * top + r] = bad ? nan : empty ? -INFINITY : (x - m) - lnS;
+}
+
+// Hands the `top` largest of n unique keys in LDS (any order) to f(rank, key), a key per thread
+// and its rank by counting the larger ones; ranks from n on get key 0.  All NT threads.
+template <int NT, class F>
+__device__ __forceinline__ void place_top(const uint64_t *keys, int n, int top, int t, F f) {
+  for (int i = t; i < n; i += NT) {
+    const uint64_t key = keys[i];
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += keys[j] > key ? 1 : 0;
+    if (rank < top) f(rank, key);
+  }
+  for (int r = n + t; r < top; r += NT) f(r, 0ull);
 }
 
 template <int DT>
@@ -303,15 +345,12 @@ __device__ __forceinline__ float logit_at(const char *row, long long v) {
 // thread, loaded one step ahead.  Past the end a group is loaded from the range's last 16
 // bytes instead and what earlier groups hold is masked, so no load is conditional or leaves
 // the range (of at least one group).
-#ifndef LP_WAVES
-#define LP_WAVES 1
-#endif
-template <int DT, bool TOP, int NT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) void k_token_logprobs(LpArgs a) {
-  constexpr int EPL = LpT<DT>::EPL, ES = LpT<DT>::ES, U = kLpSlots, NW = NT / 64;
+template <int DT, bool TOP, int NT, int U>
+__global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
+  constexpr int EPL = LpT<DT>::EPL, ES = LpT<DT>::ES, NW = NT / 64;
   __shared__ float s_m[NW], s_thr[NW];
   __shared__ double s_S[NW], s_T[NW];
-  __shared__ uint64_t s_buf[TOP ? NW * kLpBuf : 1], s_pool[TOP ? NW * 64 : 1];
+  __shared__ uint64_t s_buf[TOP ? NW * kLpBuf : 1], s_pool[TOP ? NW * kLpBuf : 1];
   __shared__ unsigned s_note[TOP ? NW * kLpNotes : 1];
   __shared__ int s_n;
 
@@ -332,9 +371,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) 
   double S = 0.0, T = 0.0;
   WaveTop wt;
   int fresh = 0;  // groups noted since the wave's threshold was last renewed
+  float run[U];   // the largest element so far at each lane and slot
+#pragma unroll
+  for (int u = 0; u < U; ++u) run[u] = -INFINITY;
   volatile float *thr_of = s_thr;
   if (TOP) {
-    wt.init(a.top, lane, s_buf + w * kLpBuf, s_note + w * kLpNotes);
+    wt.init(a.top, EPL, lane, s_buf + w * kLpBuf, s_note + w * kLpNotes);
     if (t < NW) s_thr[t] = -INFINITY;
     if (t == 0) s_n = 0;
     __syncthreads();
@@ -400,9 +442,17 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) 
   // The step's groups among the candidates; code that is kept in one place, as it is long and
   // seldom runs.
   auto choose = [&](int step, bool end) {
-    if (step == 0 || fresh >= 16) {  // the lanes' maxima have grown since the last look
-      const unsigned k = wave_sort(val_key(m > kLpNone ? m : -INFINITY), lane);
-      wt.raise(key_val(__builtin_amdgcn_readlane(k, a.top - 1)));
+#pragma unroll
+    for (int u = 0; u < U; ++u) run[u] = fmaxf(run[u], lu[u]);
+    if (step == 0 || fresh >= 16) {  // the maxima have grown since the last look
+      if (a.top <= kLpFew) {
+        float lm = run[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) lm = fmaxf(lm, run[u]);
+        wt.raise(key_val(__builtin_amdgcn_readlane(wave_sort(val_key(lm), lane), a.top - 1)));
+      } else {
+        wt.raise(wave_nth(run, a.top));
+      }
       if (lane == 0) thr_of[w] = wt.thr;
       fresh = 0;
     }
@@ -414,7 +464,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) 
       wt.look(lu[u], (unsigned)e0 + ((step * U + u) * NT + t) * EPL);
     fresh += wt.notes - before;
     if (wt.notes > kLpNotes - 64 * U || end)
-      wt.template drain<DT>((unsigned)e0 + len, [&](unsigned i) { return rp + (size_t)i * ES; });
+      wt.template drain<DT>((unsigned)e0 + len, a.S > 1 ? kLpBuf : 64, [&](unsigned i) { return rp + (size_t)i * ES; });
   };
 
   if (len >= EPL) {
@@ -449,40 +499,63 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(LP_WAVES))) 
     if (TOP) s_thr[w] = wt.thr;
   }
   __syncthreads();
+  const long long at = (long long)row * a.S + split;
   if (TOP) {
-    // the waves' candidates that reach the best threshold, at most 64 of each
+    // the waves' candidates that reach the best threshold
     float thr = s_thr[0];
 #pragma unroll
     for (int i = 1; i < NW; ++i) thr = fmaxf(thr, s_thr[i]);
-    const uint64_t key = lane < wt.cnt ? wt.buf[lane] : 0;
-    const bool in = key != 0 && key_val((unsigned)(key >> 32)) >= thr;
-    if (in) s_pool[atomicAdd(&s_n, 1)] = key;
-    __syncthreads();
+    for (int i = lane; i < wt.cnt; i += 64) {
+      const uint64_t key = wt.buf[i];
+      if (key_val((unsigned)(key >> 32)) >= thr) s_pool[atomicAdd(&s_n, 1)] = key;
+    }
   }
+  if (TOP) __syncthreads();
+  if (TOP && a.S > 1)  // `top` keys, fewer only where NaN has taken the place of values
+    place_top<NT>(s_pool, s_n, a.top, t, [&](int r, uint64_t key) { a.keys[at * a.top + r] = key; });
+  // many rows: the other waves make room for the next ones
   if (w != 0) return;
   for (int i = 1; i < NW; ++i) lp_join(m, S, T, s_m[i], s_S[i], s_T[i]);
-  uint64_t list = 0;
-  if (TOP) list = wave_best(s_pool, s_n, lane);
   if (a.S > 1) {
-    const long long at = (long long)row * a.S + split;
     if (lane == 0) a.part[at] = LpPart{S, T, m, 0};
-    if (TOP && lane < a.top) a.keys[at * a.top + lane] = list;
     return;
   }
   float lnS = 0.f;
-  if (lane == 0) lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
-  if (TOP) write_top(a.out, row, a.top, lane, list, m, __shfl(lnS, 0, 64));
+  if (lane == 0) {
+    lnS = lp_log(m, S);
+    lp_finish(a.out, row, m, S, T, lnS, tok, a.V, zt);
+  }
+  if (TOP) {
+    lnS = __shfl(lnS, 0, 64);
+    auto write = [&](int r, uint64_t key) { write_top(a.out, row, a.top, r, key, m, lnS); };
+    const int n = s_n;
+    if (n <= 64) {
+      place_top<64>(s_pool, n, a.top, lane, write);
+    } else {
+      const uint64_t list = wave_best(s_pool, n, lane);
+      if (lane < a.top) write(lane, list);
+    }
+  }
 }
 
 // Joins a row's vocabulary splits: one workgroup per row.
 constexpr int kLpMaxSplits = 64;
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kLpThreads) void k_token_logprobs_join(LpArgs a) {
-  constexpr int NW = kLpThreads / 64;
-  __shared__ uint64_t s_thr[NW], s_pool[TOP ? kLpMaxSplits * kLpMaxTop : 1];
+  constexpr int MAXK = kLpMaxSplits * kLpMaxTop, NK = MAXK / kLpThreads;
+  __shared__ uint64_t s_pool[TOP ? MAXK : 1];
+  __shared__ uint64_t s_thr[kLpThreads / 64];
+  __shared__ float s_row[2];
   __shared__ int s_n;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const long long row = blockIdx.x;
+  const int n = TOP ? a.S * a.top : 0;
+  uint64_t k[NK];
+  if (TOP) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      k[i] = i * kLpThreads + t < n ? a.keys[row * n + i * kLpThreads + t] : 0ull;
+  }
   float m = kLpNone, zt = 0.f;
   double S = 0.0, T = 0.0;
   long long tok = -1;
@@ -496,31 +569,51 @@ __global__ __launch_bounds__(kLpThreads) void k_token_logprobs_join(LpArgs a) {
     tok = a.tokens.at(row);
     if (tok >= 0 && tok < a.V)
       zt = logit_at<DT>((const char *)a.logits + row * a.ld * LpT<DT>::ES, tok);
+    if (lane == 0) s_n = 0;
   }
   if (TOP) {
-    // the top-th largest of a wave's 64 lane maxima bounds the row's top-th key from below
-    const uint64_t *k = a.keys + row * a.S * a.top;
-    const int n = a.S * a.top;
-    uint64_t best = 0;
-    for (int i = t; i < n; i += kLpThreads) best = k[i] > best ? k[i] : best;
-    best = wave_sort(best, lane);
-    if (lane == a.top - 1) s_thr[w] = best;
-    if (t == 0) s_n = 0;
+    // a value that `top` keys reach: of the maxima of a wave's 64 lanes x 4 sets of keys
+    float best[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      unsigned b = 0;
+#pragma unroll
+      for (int i = u; i < NK; i += 4) b = max(b, (unsigned)(k[i] >> 32));
+      best[u] = b ? key_val(b) : -INFINITY;
+    }
+    // (and, where many are equal, a key that `top` reach: of the maxima of its 64 lanes)
+    uint64_t bound = 1, mine = 0;
+    if (n > kLpThreads) {
+      const float v = a.top > kLpFew ? wave_nth(best, a.top) : -INFINITY;
+      bound = v > -INFINITY ? (uint64_t)val_key(v) << 32 : 1;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) mine = k[i] > mine ? k[i] : mine;
+      mine = wave_sort(mine, lane);
+    }
+    if (lane == a.top - 1) s_thr[w] = mine > bound ? mine : bound;
     __syncthreads();
     uint64_t thr = s_thr[0];
 #pragma unroll
-    for (int i = 1; i < NW; ++i) thr = s_thr[i] > thr ? s_thr[i] : thr;
-    for (int i = t; i < n; i += kLpThreads)
-      if (k[i] != 0 && k[i] >= thr) s_pool[atomicAdd(&s_n, 1)] = k[i];
-    __syncthreads();
+    for (int i = 1; i < kLpThreads / 64; ++i) thr = s_thr[i] > thr ? s_thr[i] : thr;
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      if (k[i] >= thr) s_pool[atomicAdd(&s_n, 1)] = k[i];
   }
-  if (w != 0) return;
-  wave_join(m, S, T);
-  uint64_t list = 0;
-  if (TOP) list = wave_best(s_pool, s_n, lane);
-  float lnS = 0.f;
-  if (lane == 0) lnS = lp_finish(a.out, row, m, S, T, tok, a.V, zt);
-  if (TOP) write_top(a.out, row, a.top, lane, list, m, __shfl(lnS, 0, 64));
+  if (w == 0) {
+    wave_join(m, S, T);
+    if (lane == 0) {
+      const float lnS = lp_log(m, S);
+      lp_finish(a.out, row, m, S, T, lnS, tok, a.V, zt);
+      s_row[0] = m;
+      s_row[1] = lnS;
+    }
+  }
+  if (TOP) {
+    __syncthreads();
+    place_top<kLpThreads>(s_pool, s_n, a.top, t, [&](int r, uint64_t key) {
+      write_top(a.out, row, a.top, r, key, s_row[0], s_row[1]);
+    });
+  }
 }
 
 // dz_v = p_v (g_lse - g_logp - g_entropy (ln p_v + H)) + g_logp [v = t], one thread per
@@ -616,9 +709,9 @@ template <int DT, bool TOP>
 void run_token_logprobs(const LpArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)(a.N * a.S)), rows((unsigned)a.N);
   if (a.V <= 2048)
-    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, 64>), grid, dim3(64), 0, s, a);
+    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, 64, 2>), grid, dim3(64), 0, s, a);
   else
-    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, kLpThreads>), grid, dim3(kLpThreads), 0, s, a);
+    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, kLpThreads, kLpSlots>), grid, dim3(kLpThreads), 0, s, a);
   if (a.S > 1)
     hipLaunchKernelGGL((k_token_logprobs_join<DT, TOP>), rows, dim3(kLpThreads), 0, s, a);
 }

@@ -32,16 +32,21 @@ struct LpOut {
   int bad_code;
 };
 
-// Writes a row's results from its maximum m, S = sum exp(z - m), T = sum exp(z - m)(z - m)
-// and the given token's logit zt.  No finite logit (S = 0): lse = logp = -inf, entropy 0.
-// A NaN or +inf logit (S is NaN): everything NaN.  Returns ln S, NaN for a bad row and -inf
-// for an empty one.  S >= 1 holds the maximum's own term 1: ln S keeps its digits there
-// through ln(1 + x).
-__device__ __forceinline__ float lp_finish(const LpOut &o, long long n, float m, double S,
-                                           double T, long long tok, long long V, float zt) {
+// ln S of a row with maximum m and S = sum exp(z - m): NaN for a bad row (a NaN or +inf logit),
+// -inf for an empty one (no finite logit, S = 0).  S >= 1 holds the maximum's own term 1: ln S
+// keeps its digits there through ln(1 + x).
+__device__ __forceinline__ float lp_log(float m, double S) {
+  if (!(S >= 0.0) || !(m < INFINITY)) return __uint_as_float(0x7FC00000u);
+  if (S == 0.0) return -INFINITY;
+  return S < 2.0 ? log1pf((float)(S - 1.0)) : logf((float)S);
+}
+
+// Writes a row's results from m, S, lnS = lp_log(m, S), T = sum exp(z - m)(z - m) and the given
+// token's logit zt.  An empty row has lse = logp = -inf and entropy 0, a bad one NaN.
+__device__ __forceinline__ void lp_finish(const LpOut &o, long long n, float m, double S, double T,
+                                          float lnS, long long tok, long long V, float zt) {
   const float nan = __uint_as_float(0x7FC00000u);
-  const bool bad = !(S >= 0.0) || !(m < INFINITY), empty = !bad && S == 0.0;
-  const float lnS = bad ? nan : empty ? -INFINITY : S < 2.0 ? log1pf((float)(S - 1.0)) : logf((float)S);
+  const bool bad = lnS != lnS, empty = lnS == -INFINITY;
   float lp, H, lse, mm = m;
   if (bad) {
     lp = H = lse = mm = nan;
@@ -60,7 +65,6 @@ __device__ __forceinline__ float lp_finish(const LpOut &o, long long n, float m,
   o.lse[n] = lse;
   if (o.stats) o.stats[n] = make_float2(mm, empty ? 0.f : lnS);
   if (o.status && (bad || tok >= V)) *o.status = o.bad_code;
-  return lnS;
 }
 
 // --- log probabilities from logits (kd_logprobs.hip) ---
