@@ -30,6 +30,7 @@ struct ClipTab {
   unsigned first[kTab + 1];  // first chunk of each tensor, and the end
   unsigned char bf16[kTab];
   int count;
+  int stream;                // more is written than the last-level cache holds: pass it by
   long long chunk;           // elements, a multiple of 8 * kThreads * kU
 };
 static_assert(sizeof(ClipTab) < 3500, "kernel arguments stay below 4 KB");
@@ -139,8 +140,9 @@ __global__ __launch_bounds__(kThreads) void k_norm(const double *part, long long
 
 template <int BF16>
 __device__ __forceinline__ void scale_chunk(const char *in, char *out, long long e0, long long end,
-                                            float s) {
+                                            float s, bool stream) {
   constexpr int ES = BF16 ? 2 : 4;
+  stream = stream && ((uintptr_t)out & 15) == 0;
   each_group<BF16>(in, e0, end, [&](long long e, u4 r, int n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -152,7 +154,8 @@ __device__ __forceinline__ void scale_chunk(const char *in, char *out, long long
         r[j] = __float_as_uint(__uint_as_float(r[j]) * s);
     }
     if (n == (BF16 ? 8 : 4)) {
-      __builtin_memcpy(out + e * ES, &r, 16);
+      if (stream) __builtin_nontemporal_store(r, (u4 *)(out + e * ES));
+      else __builtin_memcpy(out + e * ES, &r, 16);
     } else {
 #pragma unroll
       for (int j = 0; j < (BF16 ? 8 : 4); ++j)
@@ -175,8 +178,8 @@ __global__ __launch_bounds__(kThreads) void k_clip(ClipTab t, const double *part
   if (scale == 1.f && t.in[i] == t.out[i]) return;  // nothing changes in place
   const long long e0 = (long long)(b - t.first[i]) * t.chunk;
   const long long end = e0 + t.chunk < t.n[i] ? e0 + t.chunk : t.n[i];
-  if (t.bf16[i]) scale_chunk<1>(t.in[i], t.out[i], e0, end, scale);
-  else scale_chunk<0>(t.in[i], t.out[i], e0, end, scale);
+  if (t.bf16[i]) scale_chunk<1>(t.in[i], t.out[i], e0, end, scale, t.stream);
+  else scale_chunk<0>(t.in[i], t.out[i], e0, end, scale, t.stream);
 }
 
 // Chunks of at least 8192 elements, and longer ones once there would be more than about
@@ -201,6 +204,8 @@ hipError_t launch_clip_grads(const void *const *grads, void *const *outs, const 
                              const int32_t *dtypes, int32_t n, bool scale, float max_norm,
                              float *norm, double *part, hipStream_t s) {
   const int64_t chunk = chunk_of(numel, n), npart = clip_partials(numel, n);
+  int64_t bytes = 0;
+  for (int32_t i = 0; i < n; ++i) bytes += numel[i] * (dtypes[i] == 1 ? 2 : 4);
   for (int pass = 0; pass < (scale && npart > 0 ? 2 : 1); ++pass) {
     int64_t base = 0;
     bool first = true;
@@ -208,6 +213,7 @@ hipError_t launch_clip_grads(const void *const *grads, void *const *outs, const 
       ClipTab t;
       t.count = 0;
       t.chunk = chunk;
+      t.stream = bytes > ((int64_t)256 << 20);
       unsigned blocks = 0;
       for (; i < n && t.count < kTab; ++i) {
         if (numel[i] == 0) continue;

@@ -38,7 +38,7 @@ def check(torch, grads, max_norm, out):
 @pytest.mark.parametrize("sizes,kinds", [
     ([1], "f"), ([1], "b"), ([3, 1, 7], "bfb"), ([8191, 8192, 8193], "fbf"),
     ([100003, 5, 0, 64 * 1024], "bffb"), ([4097] * 200, "fb" * 100), ([30000001], "b"),
-    ([20000003, 77], "fb")])
+    ([20000003, 77], "fb"), ([77, 70000003], "ff")])
 def test_values(torch_cuda, sizes, kinds, factor, inplace):
     torch = torch_cuda
     grads = make(torch, sizes, kinds, sum(sizes))

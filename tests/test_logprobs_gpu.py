@@ -233,6 +233,23 @@ def test_gradient_in_place_and_into_padded_rows(torch_cuda):
     assert torch.equal(logits, x.grad) and (whole[:, 777:] == 7.0).all()
 
 
+def test_gradients_too_large_for_the_cache(torch_cuda):
+    """A gradient of more than 256 MB is stored past the cache: the same bits as in parts."""
+    torch = torch_cuda
+    for V in (128256, 128255):  # rows of an odd length are not aligned
+        z, tokens = make_rows(torch, 1100, V, torch.bfloat16, 65)
+        g = torch.randn(1100, device="cuda")
+
+        def grad(a, b):
+            x = z[a:b].detach().requires_grad_()
+            logp, H, _ = kd.token_logprobs(x, tokens[a:b])
+            return torch.autograd.grad((logp, H), x, (g[a:b], g[a:b]))[0]
+
+        whole = grad(0, 1100)
+        for a in range(0, 1100, 550):
+            assert torch.equal(whole[a:a + 550], grad(a, a + 550))
+
+
 def test_invalid_rows_have_nan_gradients(torch_cuda):
     torch = torch_cuda
     z, tokens = make_rows(torch, 4, 333, torch.float32, 71)
