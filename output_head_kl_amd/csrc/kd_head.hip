@@ -165,6 +165,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_head_join(const float2 *part,
   lanes(E < 64 ? E : 64);
   if (lane >= TOK || r >= rows) return;
   const long long tok = tokens.at(r);
+  if (T != T) S = T;  // a logit that is not finite
   lp_finish(out, r, m, S, T, lp_log(m, S), tok, V, tok >= 0 && tok < V ? zt[r] : 0.f);
 }
 

@@ -96,6 +96,20 @@ def test_gradients(torch_cuda, dtype, N, d, V, chunk, which):
         assert (hx.grad[1] == 0).all()  # no token: no gradient
 
 
+def test_infinite_logits_make_the_row_invalid(torch_cuda):
+    """An infinite weight: -inf or +inf logits, so NaN in the row's results, status set."""
+    torch = torch_cuda
+    for N, V in ((3, 500), (3, 70000), (300, 500)):
+        for sign in (-1.0, 1.0):
+            h, W, tokens = make(torch, N, 64, V, "bf16", 5)
+            h[:, 0] = 1.0
+            W[V // 2, 0] = sign * float("inf")
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            for out in kd.head_logprobs(h, W, tokens, status=status):
+                assert out.isnan().all(), (N, V, sign)
+            assert status.item() == 2
+
+
 @pytest.mark.parametrize("size", [9.0, 16.0])
 def test_confident_tokens_keep_their_small_gradients(torch_cuda, size):
     """p of the given token near one: its dz = g (1 - p) is rounded once, not a difference of
