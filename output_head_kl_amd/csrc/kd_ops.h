@@ -107,6 +107,16 @@ struct HeadCoef {  // per token of a chunk
 };
 hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows, int64_t V,
                             const HeadCoef &k, hipStream_t s);
+// Few tokens in bf16: dz (null: not wanted; 2 * head_few_tokens * V_pad elements) in the order
+// that launch_head_few_dh reads, and dW of type out (null: not wanted); V_pad a multiple of 256,
+// ht as launch_transpose_h leaves it.  part: nsplit * head_few_tokens * (d rounded to 128).
+inline int head_few_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int head_few_dh_splits(int64_t d, int64_t V);
+hipError_t launch_head_few_bwd(const void *W, const void *h, const void *ht, int64_t rows,
+                               int64_t d, int64_t V, int64_t V_pad, const HeadCoef &k, void *dz,
+                               void *dW, int out, hipStream_t s);
+hipError_t launch_head_few_dh(const void *W, const void *dz, int64_t rows, int64_t d, int64_t V,
+                              int64_t V_pad, int nsplit, float *part, void *dh, hipStream_t s);
 // dz as blocks of 256 vocabulary columns (element (c, v) at (v / 256) * C_alloc * 256 + c * 256
 // + v % 256) and, bf16 and wanted, dzT (element (v, c) at (c / 256) * tst + v * 256 + c % 256).
 hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t rows, int64_t d,

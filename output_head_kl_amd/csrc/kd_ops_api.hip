@@ -94,6 +94,7 @@ HeadFwd head_fwd_layout(int64_t N, int64_t V, int64_t chunk, int dtype) {
 struct HeadBwd {
   int64_t C, C_alloc, V_pad, d_pad, nchunks, group, k_split;
   int nsplit;
+  bool few; // bf16, few tokens in all: one pass over W gives dz and dW
   bool wt;  // bf16: the dh product reads a k-contiguous copy of W
   size_t off_coef, off_dz, off_dhpart, off_wt, off_dzt, off_ht, off_acc, total;
 };
@@ -102,14 +103,17 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, int dtyp
   HeadBwd L;
   const bool bf16 = dtype == KD_BF16;
   const int64_t es = bf16 ? 2 : 4, n = N > 0 ? N : 1;
-  L.C = chunk < n ? chunk : n;
+  L.few = bf16 && n <= kd::kHeadFewTokens;
+  L.C = chunk < n && !L.few ? chunk : n;
   L.C_alloc = rup(L.C, kd::kTile);
-  L.V_pad = rup(V, bf16 ? 3 * kd::kTile : kd::kTile);
+  L.V_pad = rup(V, bf16 && !L.few ? 3 * kd::kTile : kd::kTile);
   L.d_pad = rup(d, kd::kTile);
   L.nchunks = (n + L.C - 1) / L.C;
   L.group = !bf16 || group < 1 ? 1 : group < L.nchunks ? group : L.nchunks;
   L.wt = bf16 && kd::head_wt(N);
-  kd::head_dh_splits(dtype, L.wt, L.C_alloc, d, L.V_pad, &L.nsplit, &L.k_split);
+  if (L.few) L.nsplit = kd::head_few_dh_splits(d, V);
+  else kd::head_dh_splits(dtype, L.wt, L.C_alloc, d, L.V_pad, &L.nsplit, &L.k_split);
+  const int64_t tok = kd::head_few_tokens(n);
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t o = off;
@@ -117,10 +121,11 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, int dtyp
     return o;
   };
   L.off_coef = take(5 * L.C_alloc * 4);
-  L.off_dz = take(L.C_alloc * L.V_pad * es);
-  L.off_dhpart = take(want_dh ? L.nsplit * L.C_alloc * L.d_pad * 4 : 0);
+  L.off_dz = take(!L.few ? L.C_alloc * L.V_pad * es : want_dh ? 2 * tok * L.V_pad * 2 : 0);
+  L.off_dhpart =
+      take(!want_dh ? 0 : L.nsplit * 4 * (L.few ? tok * rup(d, 128) : L.C_alloc * L.d_pad));
   L.off_wt = take(want_dh && L.wt ? L.V_pad * d * 2 : 0);
-  L.off_dzt = take(want_dw && bf16 ? L.group * L.C_alloc * L.V_pad * 2 : 0);
+  L.off_dzt = take(want_dw && bf16 && !L.few ? L.group * L.C_alloc * L.V_pad * 2 : 0);
   L.off_ht = take(want_dw && bf16 ? L.group * L.C_alloc * d * 2 : 0);
   L.off_acc = take(want_dw && dw_dtype != KD_F32 && L.group < L.nchunks ? V * d * 4 : 0);
   L.total = off;
@@ -372,6 +377,20 @@ int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void
   float *dhpart = (float *)(ws + L.off_dhpart);
   if (dh && WT)
     LAUNCH(kd::KC_TRANSPOSE, kd::launch_transpose_w(W, V, d, L.V_pad, WT, stream));
+  if (L.few) {
+    const kd::LpGrad g{(const float2 *)row_stats, entropy, grad_logp, grad_entropy, grad_lse};
+    void *ht = ws + L.off_ht;
+    LAUNCH(kd::KC_LOGPROBS_BWD,
+           kd::launch_head_coef(tokens_at(tokens, token_bits, 0), g, N, V, k, stream));
+    if (dW) LAUNCH(kd::KC_TRANSPOSE, kd::launch_transpose_h(h, N, d, L.C_alloc, ht, tst_h, stream));
+    LAUNCH(kd::KC_BWD_GEMM,
+           kd::launch_head_few_bwd(W, h, ht, N, d, V, L.V_pad, k, dh ? dz : nullptr, dW, dw_dtype,
+                                   stream));
+    if (dh)
+      LAUNCH(kd::KC_DH_GEMM, kd::launch_head_few_dh(W, dz, N, d, V, L.V_pad, L.nsplit, dhpart, dh,
+                                                    stream));
+    return KD_OK;
+  }
   int64_t chunk_i = 0;
   float *sum = nullptr;  // the earlier groups' sum
   for (int64_t c0 = 0; c0 < N; c0 += L.C, ++chunk_i) {

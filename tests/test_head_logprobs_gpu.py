@@ -96,6 +96,44 @@ def test_gradients(torch_cuda, dtype, N, d, V, chunk, which):
         assert (hx.grad[1] == 0).all()  # no token: no gradient
 
 
+@pytest.mark.parametrize("dw", ["bf16", "f32"])
+@pytest.mark.parametrize("N,d,V", [(1, 8, 3), (1, 1000, 513), (5, 136, 2050), (16, 520, 700),
+                                   (17, 264, 3001), (33, 1032, 1111), (48, 64, 20000),
+                                   (64, 264, 5003)])
+def test_few_tokens_gradients_are_rounded_once(torch_cuda, N, d, V, dw):
+    """bf16, up to 64 tokens: dz enters the products to 2^-16 of its size (a bf16 number and
+    the bf16 of what it leaves), so an element of dh or dW is off by one rounding to its type
+    plus that, z's own error through p, and the float32 sums' (of random sign, so 6 sqrt n U of
+    the terms' sizes for n of them)."""
+    torch = torch_cuda
+    h, W, tokens = make(torch, N, d, V, "bf16", 77 + N)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    gl, ge, gz = (torch.randn(N, generator=g, device="cuda") for _ in range(3))
+    outs = kd._ops._head_logprobs(h, W, tokens, 4096, None, None, True)
+    dt = torch.bfloat16 if dw == "bf16" else torch.float32
+    dh, dW = kd.head_logprobs_bwd(h, W, tokens, outs[1], outs[0][1], gl, ge, gz, dW_dtype=dt)
+    assert dW.dtype == dt
+    hn, Wn, tk = np64(h), np64(W), tokens.cpu().numpy()
+    z = hn @ Wn.T
+    f = ref.forward(z, tk)
+    dz = ref.gradient(z, tk, np64(gl), np64(ge), np64(gz))
+    lp = z - f["lse"][:, None]
+    tl, th = row_tolerances(z)
+    ez = z_tolerance(hn, Wn) + 4 * U * np.abs(z).max(1)
+    size = (np.abs(np64(gl)) + np.abs(np64(gz)))[:, None] + \
+        np.abs(np64(ge))[:, None] * (np.abs(lp) + f["entropy"][:, None] + 1)
+    A = (np.exp(lp) * np.abs(z - z.max(1)[:, None])).sum(1) + f["entropy"] + 2
+    err = np.exp(lp) * size * (2 * ez * A + tl + th + 16 * U)[:, None] + 2.0 ** -16 * np.abs(dz)
+    err[np.arange(N)[tk >= 0], tk[tk >= 0]] += 2 * U * np.abs(np64(gl))[tk >= 0]
+    mag = np.abs(dz) + err
+    for name, got, want, e, half in (
+            ("dh", dh, dz @ Wn, err @ np.abs(Wn) + 6 * V ** 0.5 * U * (mag @ np.abs(Wn)), 2.0 ** -8),
+            ("dW", dW, dz.T @ hn, err.T @ np.abs(hn) + 6 * (2 * N) ** 0.5 * U * (mag.T @ np.abs(hn)),
+             2.0 ** -8 if dw == "bf16" else U)):
+        off = np.abs(np64(got) - want) - half * (np.abs(want) + e) - e
+        assert off.max() <= 0, f"{name}: {off.max():.3g} past the tolerance"
+
+
 def test_infinite_logits_make_the_row_invalid(torch_cuda):
     """An infinite weight: -inf or +inf logits, so NaN in the row's results, status set."""
     torch = torch_cuda
