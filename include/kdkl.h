@@ -406,7 +406,8 @@ int kd_token_logprobs(const void *logits, int32_t dtype, int64_t ld, const void 
  *   dlogits [N] rows of V elements of dtype, ld_d elements apart; rounded once (RNE); may be
  *           logits itself (same address and, when N > 1, ld_d == ld), may not overlap it
  *           otherwise.  Elements between V and ld_d are left as they were.
- * Limits, stream behaviour and errors as kd_token_logprobs; no workspace.
+ * Limits, stream behaviour and errors as kd_token_logprobs (and fewer than 2^24 pieces of
+ * 16 KB in all rows); no workspace.
  */
 int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const void *tokens,
                           int32_t token_bits, int64_t N, int64_t V, const float *row_stats,
@@ -425,17 +426,19 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
  * Products are exact and summed in float32.  A row whose logits are not all finite gets NaN.
  *
  * kd_head_logprobs_bwd: for upstream gradients gl, ge, gz of logp, entropy and row_lse
- *   ([N] float32; NULL = 0), with dz as in kd_token_logprobs_bwd (rounded to dtype once):
+ *   ([N] float32; NULL = 0), with dz as in kd_token_logprobs_bwd (rounded to dtype
+ *   once; up to 64 tokens in bf16 kept as two bf16 numbers, to 2^-16 of its size):
  *   dh = dz W  [N, d] dtype, rounded once;  dW = dz^T h  [V, d] dw_dtype (KD_F32 or dtype),
- *   overwritten, rounded once (each 16-byte aligned; either may be NULL: not wanted)
+ *   overwritten, rounded once (each 16-byte aligned; either may be NULL: not wanted; not in
+ *   the memory of h, W or each other)
  *   row_stats, entropy  from kd_head_logprobs on the same h and W
  *   workspace  kd_head_logprobs_bwd_workspace_bytes(..., 16384, ...) bytes for full speed, at
  *              least (..., 0, ...) bytes; dw_group_tokens as kd_workspace_bytes_group
  * A token >= V makes its row of dh and all of dW NaN.
  *
  * Sizes: N >= 0, d >= 8 with d % 8 == 0, d <= 2^20, 1 <= V <= 2^24, chunk >= 1, min(chunk, N)
- * <= 2^22.  Results do not depend on timing, and on chunk only in the order of float32 sums.  No
- * synchronisation, copy or allocation: every call can be recorded into a HIP graph.
+ * <= 2^22 and min(chunk, N) V <= 2^38.  Results do not depend on timing, and on chunk only in
+ * the order of float32 sums.  No synchronisation, copy or allocation: every call can be recorded into a HIP graph.
  */
 int kd_head_logprobs_workspace_bytes(int64_t N, int64_t d, int64_t V, int64_t chunk,
                                      int32_t dtype, size_t *bytes_out);

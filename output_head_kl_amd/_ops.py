@@ -1,7 +1,8 @@
-"""The operators beside the loss: log probabilities of given tokens (from logits
-and from hidden states) with their gradients, and the gradient norm with clipping.  Thin, as the rest of the binding: arguments are checked, outputs and workspaces
-allocated with torch, and the library's HIP kernels do the work on the current stream (or on
-``stream``).  No call synchronises, so each can be recorded with ``torch.cuda.graph``."""
+"""The operators beside the loss: log probabilities of given tokens (from logits and from
+hidden states) with their gradients, and the gradient norm with clipping.  Thin, as the rest
+of the binding: arguments are checked, outputs and workspaces allocated with torch, and the
+library's HIP kernels do the work on the current stream (or on ``stream``).  No call
+synchronises, so each can be recorded with ``torch.cuda.graph``."""
 from __future__ import annotations
 
 import array
@@ -142,6 +143,8 @@ def _token_logprobs(logits, tokens, top, status, workspace, stats):
     dev = logits.device
     _same_device(dev, tokens=tokens, status=status)
     N, V, ld = _rows(logits, "logits")
+    if not 0 <= top <= V:
+        raise ValueError(f"top = {top} outside [0, {V}]")
     bits = _token_bits(tokens, N)
     workspace = _scratch(workspace, token_logprobs_workspace_bytes(N, V, top, dt), dev)
     logp = torch.empty(N, dtype=_F32, device=dev)
@@ -334,10 +337,10 @@ def head_logprobs_bwd(h, W, tokens, row_stats, entropy, grad_logp=None, grad_ent
                       grad_lse=None, chunk: int = 4096, want_dh: bool = True,
                       want_dW: bool = True, dW_dtype=torch.float32,
                       dw_group_tokens: int = 16384, workspace=None, stream=None):
-    """(dh [N, d] in h's dtype, dW [V, d] in ``dW_dtype``, float32 or h's) of ``head_logprobs`` for upstream gradients
-    [N] of logp, entropy and lse (None: 0); None for the one that is not wanted.  ``row_stats``
-    [N, 2] and ``entropy`` [N] come from the forward; ``workspace`` and ``dw_group_tokens`` as
-    in ``fwd_bwd``."""
+    """(dh [N, d] in h's dtype, dW [V, d] in ``dW_dtype``, float32 or h's) of ``head_logprobs``
+    for upstream gradients [N] of logp, entropy and lse (None: 0); None for the one that is not
+    wanted.  ``row_stats`` [N, 2] and ``entropy`` [N] come from the forward; ``workspace`` and
+    ``dw_group_tokens`` as in ``fwd_bwd``."""
     dev = h.device
     kd._on_device(dev, h=h)
     if _elsewhere(dev, stream):

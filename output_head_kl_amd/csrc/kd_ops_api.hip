@@ -51,6 +51,9 @@ int check_head(const void *h, const void *W, int32_t dtype, const void *tokens, 
     return set_error(KD_E_UNSUPPORTED, "d must be at most 2^20, V 2^24 and N 2^40");
   if ((chunk < N ? chunk : N) > ((int64_t)1 << 22))
     return set_error(KD_E_UNSUPPORTED, "min(chunk, N) must be at most 2^22 rows");
+  // a launch has fewer than 2^32 threads
+  if ((chunk < N ? chunk : N) * V > ((int64_t)1 << 38))
+    return set_error(KD_E_UNSUPPORTED, "min(chunk, N) x V must be at most 2^38");
   if (!pointers) return KD_OK;
   if (token_bits != 32 && token_bits != 64)
     return set_error(KD_E_ARG, "token_bits = %d: tokens are 32- or 64-bit integers", token_bits);
@@ -59,6 +62,11 @@ int check_head(const void *h, const void *W, int32_t dtype, const void *tokens, 
   if (mis(h, 16) || mis(W, 16)) return set_error(KD_E_ARG, "h and W must be 16-byte aligned");
   if (mis(tokens, token_bits / 8)) return set_error(KD_E_ARG, "tokens misaligned");
   return KD_OK;
+}
+
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
 int check_workspace(const void *workspace, size_t bytes, size_t need) {
@@ -261,8 +269,8 @@ int kd_token_logprobs_bwd(const void *logits, int32_t dtype, int64_t ld, const v
   const uintptr_t na = (uintptr_t)(((N - 1) * ld + V) * es), nb = (uintptr_t)(((N - 1) * ld_d + V) * es);
   if (a < b + nb && b < a + na && !(a == b && (N == 1 || ld == ld_d)))
     return set_error(KD_E_ARG, "dlogits overlaps logits and is not logits itself");
-  // one workgroup per 8192 bf16 or 4096 fp32 elements of a row
-  if (N * ((V * es + 16383) / 16384) > (int64_t)0x7FFFFFFF)
+  // one workgroup of 256 per 8192 bf16 or 4096 fp32 elements of a row: fewer than 2^32 threads
+  if (N * ((V * es + 16383) / 16384) >= ((int64_t)1 << 24))
     return set_error(KD_E_UNSUPPORTED, "N x V is too large for one call");
   hipStream_t stream = (hipStream_t)stream_v;
   const kd::LpGrad g{(const float2 *)row_stats, entropy, grad_logp, grad_entropy, grad_lse};
@@ -362,6 +370,12 @@ int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void
   if (rc != KD_OK) return rc;
   hipStream_t stream = (hipStream_t)stream_v;
   const bool bf16 = dtype == KD_BF16;
+  // a chunk's results are written before the next one reads h and W
+  const int64_t nh = N * d * (bf16 ? 2 : 4), nW = V * d * (bf16 ? 2 : 4);
+  const int64_t nG = V * d * (dw_dtype == KD_F32 ? 4 : 2);
+  if (overlap(dh, nh, h, nh) || overlap(dh, nh, W, nW) || overlap(dW, nG, h, nh) ||
+      overlap(dW, nG, W, nW) || overlap(dh, nh, dW, nG))
+    return set_error(KD_E_ARG, "dh and dW may not share memory with h, W or each other");
   const int64_t es = bf16 ? 2 : 4, tst_dz = L.V_pad * 256, tst_h = d * 256;
   if (N == 0) {
     if (dW)

@@ -47,6 +47,19 @@ def test_backward_refusals(change, code):
     assert bwd(**change) == code and kd._lib().kd_last_error() != b""
 
 
+@pytest.mark.parametrize("place", ["h in dh", "W in dh", "h in dW", "W in dW", "dh in dW"])
+def test_results_in_the_operands_are_refused(place):
+    far = {name: 1 << (30 + 2 * i) for i, name in enumerate(("h", "W", "dh", "dW"))}
+    inner, outer = place.split(" in ")
+    at = dict(far, **{inner: far[outer] + 128})  # inside the other's 4 x 64 or 64 x 64 elements
+    assert bwd(**at) == E_ARG and b"share memory" in kd._lib().kd_last_error()
+
+
+def test_more_threads_than_a_launch_has_are_refused():
+    for f in (fwd, bwd):
+        assert f(N=1 << 22, chunk=1 << 22, V=(1 << 16) + 1) == E_UNSUPPORTED
+
+
 def test_no_rows_need_nothing():
     assert fwd(N=0, h=None, tokens=None, logp=None, entropy=None, lse=None) == OK
     assert bwd(N=0, h=None, tokens=None, stats=None, entropy=None, dW=None) == OK

@@ -76,6 +76,11 @@ def test_backward_refusals(lib, change, code):
     assert _bwd(lib, **change) == code
 
 
+def test_more_threads_than_a_launch_has_are_refused(lib):
+    """(2^24 - 1) rows of two pieces of 8192 elements, 256 threads each: over 2^32."""
+    assert _bwd(lib, N=(1 << 24) - 1, V=8193, ld=8200, ld_d=8200, out=1 << 62) == E_UNSUPPORTED
+
+
 def test_no_rows_need_nothing(lib):
     assert _fwd(lib, N=0, logits=None, tokens=None, logp=None, entropy=None, lse=None, idx=None,
                 tlp=None, ws=None) == OK
