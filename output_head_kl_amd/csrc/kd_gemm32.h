@@ -40,27 +40,30 @@ __device__ __forceinline__ void chunk(int q, int &mn, int &k, int &at) {
 }
 
 // k and mn extents are multiples of 4 in the contiguous direction, so a chunk is inside or not.
+// One outside is loaded from the last place inside and becomes zero on its way to LDS: a load
+// under a condition would be waited for at once.
 template <int T, int KIND>
 __device__ __forceinline__ void load(u32x4 (&r)[T / 32], const Operand &op, int mn0, int k0, int t) {
+  const int last_mn = op.mn_ext - (KIND == OP_KC ? 1 : 4), last_k = op.k_ext - (KIND == OP_KC ? 4 : 1);
 #pragma unroll
   for (int i = 0; i < T / 32; ++i) {
     int mn, k, at;
     chunk<T, KIND>(t + 256 * i, mn, k, at);
-    mn += mn0;
-    k += k0;
-    r[i] = u32x4{0u, 0u, 0u, 0u};
-    if (mn < op.mn_ext && k < op.k_ext)
-      r[i] = *(const u32x4 *)((const float *)op.ptr + op_index(op, KIND, mn, k));
+    r[i] = *(const u32x4 *)((const float *)op.ptr +
+                            op_index(op, KIND, min(mn + mn0, last_mn), min(k + k0, last_k)));
   }
 }
 
 template <int T, int KIND>
-__device__ __forceinline__ void store(char *lds, const u32x4 (&r)[T / 32], int t) {
+__device__ __forceinline__ void store(char *lds, const u32x4 (&r)[T / 32], const Operand &op,
+                                      int mn0, int k0, int t) {
 #pragma unroll
   for (int i = 0; i < T / 32; ++i) {
     int mn, k, at;
     chunk<T, KIND>(t + 256 * i, mn, k, at);
-    *(LDS_AS u32x4 *)((LDS_AS char *)lds + at) = r[i];
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    *(LDS_AS u32x4 *)((LDS_AS char *)lds + at) =
+        mn + mn0 < op.mn_ext && k + k0 < op.k_ext ? r[i] : zero;
   }
 }
 
@@ -101,15 +104,14 @@ __global__ __launch_bounds__(256, 2) void gemm32_kernel(Operand A, Operand B, Ge
   u32x4 ra[T / 32], rb[T / 32];
   load<T, AK>(ra, A, m0, kb, t);
   load<T, BKIND>(rb, B, n0, kb, t);
-  store<T, AK>(smem, ra, t);
-  store<T, BKIND>(smem + AB, rb, t);
+  store<T, AK>(smem, ra, A, m0, kb, t);
+  store<T, BKIND>(smem + AB, rb, B, n0, kb, t);
   __syncthreads();
   for (int it = 0; it < nk; ++it) {
-    const bool more = it + 1 < nk;
-    if (more) {
-      load<T, AK>(ra, A, m0, kb + (it + 1) * BK, t);
-      load<T, BKIND>(rb, B, n0, kb + (it + 1) * BK, t);
-    }
+    const int k1 = kb + (it + 1) * BK;
+    load<T, AK>(ra, A, m0, k1, t);  // past the last step: loaded, not stored
+    load<T, BKIND>(rb, B, n0, k1, t);
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out before the step's products
     const char *la = smem + (it & 1) * STAGE, *lb = la + AB;
 #pragma unroll
     for (int ks = 0; ks < BK / 8; ++ks) {
@@ -123,10 +125,11 @@ __global__ __launch_bounds__(256, 2) void gemm32_kernel(Operand A, Operand B, Ge
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = mma(fa[i], fb[j], acc[i][j]);
     }
-    if (more) {
+    __builtin_amdgcn_sched_barrier(0);
+    if (it + 1 < nk) {
       char *nxt = smem + ((it + 1) & 1) * STAGE;
-      store<T, AK>(nxt, ra, t);
-      store<T, BKIND>(nxt + AB, rb, t);
+      store<T, AK>(nxt, ra, A, m0, k1, t);
+      store<T, BKIND>(nxt + AB, rb, B, n0, k1, t);
     }
     __syncthreads();
   }
