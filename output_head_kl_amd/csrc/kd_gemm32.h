@@ -3,11 +3,13 @@
 //
 // D[m][n] = sum_k A[m][k] B[k][n], operands and epilogues as in kd_gemm.h.  Four waves of T/2 x
 // T/2 (one or two by two blocks of the 32x32x2 MFMA, 64 cycles each), k in steps of 32, two LDS
-// stages filled through registers: reads, loads and barriers all take a small part of the
-// matrix instructions' time.  The 256 x 256 tile of kd_gemm.h reaches 121 TFLOP/s on large
-// shapes, this one 104 to 111 (4096 tokens, d 1024, V 32000), but small shapes fill the chip:
-// 512 tokens, d 256, V 8192 take 33 us forward instead of 84.  Below two workgroups of 128 x
-// 128 per compute unit the 64 x 64 tile is taken.
+// stages filled through registers: bound by the matrix instructions.  The next stage's loads go
+// out before a step's products and reach LDS half-way through them, fragments are read one
+// eighth of k ahead.  4096 tokens, d 1024, V 32000 run at 123 TFLOP/s forward and 120 over the
+// three products of the gradients (a library's plain product of that shape at 140, the 256 x
+// 256 tile of kd_gemm.h at 121), but small shapes fill the chip: 512 tokens, d 256, V 8192 take
+// 29 us forward instead of 84.  Below two workgroups of 128 x 128 per compute unit the 64 x 64
+// tile is taken.
 #pragma once
 
 #include "kd_gemm.h"
@@ -16,7 +18,8 @@ namespace kd {
 namespace g32 {
 
 constexpr int BK = 32;
-// KC: [T rows][128 B], 16-byte chunks swizzled by row; MC: [32 k][T mn], padded rows
+// KC: [T rows][128 B], 16-byte chunks swizzled by row so that 16 rows' chunks of a fragment fall
+// on all 64 banks; MC: [32 k][T mn], padded rows
 template <int T> constexpr int mc_pitch() { return T * 4 + 16; }
 template <int T, int KIND> constexpr int bytes() {
   return KIND == OP_KC ? T * BK * 4 : BK * mc_pitch<T>();
@@ -31,7 +34,7 @@ __device__ __forceinline__ void chunk(int q, int &mn, int &k, int &at) {
   if (KIND == OP_KC) {
     mn = q >> 3;
     k = (q & 7) * 4;
-    at = mn * 128 + (((q & 7) ^ (mn & 7)) << 4);
+    at = mn * 128 + (((q & 7) ^ (mn >> 1 & 7)) << 4);
   } else {
     k = q / (T / 4);
     mn = (q % (T / 4)) * 4;
@@ -74,7 +77,7 @@ __device__ __forceinline__ f32x4 frag(const char *lds, int r0, int ks, int lane)
   const int row = r0 + (lane & 31);
   if (KIND == OP_KC) {
     const int kc = ks * 2 + (lane >> 5);
-    return *(const LDS_AS f32x4 *)(b + row * 128 + ((kc ^ (row & 7)) << 4));
+    return *(const LDS_AS f32x4 *)(b + row * 128 + ((kc ^ (row >> 1 & 7)) << 4));
   }
   const int k = ks * 8 + (lane >> 5) * 4;
   f32x4 v;
@@ -113,23 +116,29 @@ __global__ __launch_bounds__(256, 2) void gemm32_kernel(Operand A, Operand B, Ge
     load<T, BKIND>(rb, B, n0, k1, t);
     __builtin_amdgcn_sched_barrier(0);  // the loads go out before the step's products
     const char *la = smem + (it & 1) * STAGE, *lb = la + AB;
+    f32x4 fa[2][NB], fb[2][NB];
+    auto frags = [&](int ks) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        fa[ks & 1][i] = frag<T, AK>(la, wr * (T / 2) + i * 32, ks, lane);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        fb[ks & 1][j] = frag<T, BKIND>(lb, wc * (T / 2) + j * 32, ks, lane);
+    };
+    frags(0);
 #pragma unroll
     for (int ks = 0; ks < BK / 8; ++ks) {
-      f32x4 fa[NB], fb[NB];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) fa[i] = frag<T, AK>(la, wr * (T / 2) + i * 32, ks, lane);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) fb[j] = frag<T, BKIND>(lb, wc * (T / 2) + j * 32, ks, lane);
+      if (ks + 1 < BK / 8) frags(ks + 1);
+      if (ks == BK / 16 && it + 1 < nk) {  // between products, so they cover its waits
+        char *nxt = smem + ((it + 1) & 1) * STAGE;
+        store<T, AK>(nxt, ra, A, m0, k1, t);
+        store<T, BKIND>(nxt + AB, rb, B, n0, k1, t);
+      }
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mma(fa[i], fb[j], acc[i][j]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (it + 1 < nk) {
-      char *nxt = smem + ((it + 1) & 1) * STAGE;
-      store<T, AK>(nxt, ra, A, m0, k1, t);
-      store<T, BKIND>(nxt + AB, rb, B, n0, k1, t);
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = mma(fa[ks & 1][i], fb[ks & 1][j], acc[i][j]);
     }
     __syncthreads();
   }
