@@ -96,6 +96,18 @@ def test_gradients(torch_cuda, dtype, N, d, V, chunk, which):
         assert (hx.grad[1] == 0).all()  # no token: no gradient
 
 
+@pytest.mark.parametrize("N,d,V,chunk", [
+    (300, 72, 70001, 2048),  # vocabulary tiles of 384 rows, a ragged last one
+    (700, 264, 40000, 300),  # the same in three chunks, the last of 100 rows
+    (1100, 264, 2050, 1100),  # dh from a copy of W: one tile of 384 hidden units
+    (1100, 512, 2050, 600),  # two of 256, two chunks of different length
+    (1030, 1000, 1999, 515)])
+def test_tiles_of_both_heights(torch_cuda, N, d, V, chunk):
+    """bf16 above 64 tokens: the products choose 256 or 384 rows of W (or of its copy) a tile."""
+    test_forward(torch_cuda, "bf16", N, d, V, chunk)
+    test_gradients(torch_cuda, "bf16", N, d, V, chunk, "all")
+
+
 @pytest.mark.parametrize("dw", ["bf16", "f32"])
 @pytest.mark.parametrize("N,d,V", [(1, 8, 3), (1, 1000, 513), (5, 136, 2050), (16, 520, 700),
                                    (17, 264, 3001), (33, 1032, 1111), (48, 64, 20000),
