@@ -176,7 +176,8 @@ def token_logprobs(logits, tokens, top: int = 0, status=None, workspace=None, st
     int32, top_logp [N, top] float32), the largest logits first, equal ones by rising index.
     logp is 0 without a token; a row with no finite logit has logp = lse = -inf, entropy 0; an
     invalid row NaN.  logp, entropy and lse are differentiable in logits (the alternatives are
-    not); the backward reads logits again."""
+    not); the backward reads logits again.  Before a backward is captured into a graph, drop
+    eager results of the same leaf (or detach it): torch fails on their streams otherwise."""
     dev = logits.device
     kd._on_device(dev, logits=logits)
     if _elsewhere(dev, stream):
@@ -322,7 +323,7 @@ def head_logprobs(h, W, tokens, chunk: int = 4096, status=None, workspace=None, 
     chunk: token rows per pass; status, stream: as ``token_logprobs``; workspace: optional
     uint8 tensor of ``head_logprobs_workspace_bytes`` bytes.
     Returns (logp [N], entropy [N], lse [N]) float32, differentiable in h and W: the backward
-    recomputes the logits chunk by chunk."""
+    recomputes the logits chunk by chunk.  Capturing it: as ``token_logprobs``."""
     dev = h.device
     kd._on_device(dev, h=h)
     if _elsewhere(dev, stream):

@@ -7,6 +7,10 @@
 //            holds it; k_head_join folds the partials into logp, entropy and lse.
 //  gradient  z again, then dz = p (gz - gl - ge (ln p + H)) + gl [v = t] in one rounding, in
 //            the layouts the dh and dW GEMMs of the loss read.
+//
+// Up to 64 tokens go the ways of kd_head_few.hip.  Above, the products bound the time: 4096
+// tokens, d 2880, V 201088 in bf16 take 3.5 ms forward (1350 TFLOP/s) and 12.0 ms for the
+// gradients: z again 3.9, dh 3.6 with the partials' sum, W's copy for it 0.5, dW 4.0.
 #include "kd_gemm.h"
 #include "kd_gemm32.h"
 #include "kd_ops.h"
@@ -90,7 +94,9 @@ struct EpiHeadFwd {
 
 // Joins a token's partials, in a fixed order: TOK tokens per workgroup (8, for 64-byte reads
 // where a partial's tokens lie side by side; 1 where a token's partials do), 1024 / TOK
-// threads per token, each up to eight partials at a time; then lanes, then waves.
+// threads per token, each up to eight partials at a time; then lanes, then waves.  Reads 12
+// bytes per partial: 24 us for 4096 tokens of 1048 partials (2.1 TB/s), 5 us, a launch's
+// latency, for 48.
 constexpr int kJoinThreads = 1024;
 __device__ __forceinline__ void head_join(float &m, double &S, double &T, float m2, double S2,
                                           double T2) {

@@ -8,8 +8,10 @@
 // them (LDS counts apart) then does not wait for W.  The k order within a fragment is the
 // memory's on both sides, which is all a dot product needs.  Per workgroup and token one
 // (max, S = sum 2^t, sum t 2^t) partial, t = (z - max) log2 e, as in kd_head.hip.
-// With one token of d 4096 over 128256 rows (1.05 GB) the call takes 194 us, 5.4 TB/s; the
-// 256-column GEMM tile takes 306 us there and 335 us for 48 tokens of d 2880 over 201088 rows.
+// With one token of d 4096 over 128256 rows (1.05 GB) the call takes 198 us, 5.3 TB/s; 48 tokens
+// of d 2880 over 201088 rows (1.16 GB) 245 us, 4.7 TB/s.  The GEMM tiles of more tokens are
+// bound by W too there (64 tokens of d 4096 this way 226 us, 65 the other 229), but take longer
+// where W is small (64 tokens, d 1024, V 32000: 22 us; 65: 34).
 // W through an LDS ring instead (loads of whole lines straight into it) measured 215 and 273 us,
 // non-temporal loads of W 212 and 302 us (a line's second half is then fetched twice).
 #include "kd_gemm.h"

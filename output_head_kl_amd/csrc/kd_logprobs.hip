@@ -5,6 +5,12 @@
 //   lse = m + ln S,  ln p_v = z_v - m - ln S,  H = -sum p ln p = ln S - T / S.
 // One pass: every lane keeps its own (m, S, T) and rescales the sums when its maximum
 // rises; lanes, waves and vocabulary splits are joined by the same rule in double.
+//
+// Bound by reading the logits once: 4096 rows of 128256 bf16 logits (1.05 GB) take 181 us, 5.8
+// TB/s, and 204 us with 8 alternatives; 1037 rows of 32003 float32 logits, a third of them
+// masked, 26 us (5.1 TB/s).  Few rows are bound by latency: one row of 128256 takes 5.3 us in
+// two launches (the splits and their join), 13.8 us with 20 alternatives, whose selection is a
+// chain of sorting steps in each.
 #include "kd_ops.h"
 
 #include <cstdint>
@@ -634,6 +640,9 @@ struct LpBwdArgs {
 // 322 us instead of 371 (2.1 GB, 6.5 TB/s); results that fit are left in it.
 constexpr int64_t kLpCache = (int64_t)256 << 20;
 
+// One workgroup per kLpSlots * kLpThreads * 16 bytes of a row: dz = p (gz - gl - ge (ln p + H))
+// + gl [v = t] from the forward's (m, ln S) and H, rounded once; p = exp((z - m) - ln S), so
+// that no large number is subtracted from another.
 template <int DT>
 __global__ __launch_bounds__(kLpThreads) void k_token_logprobs_bwd(LpBwdArgs a) {
   constexpr int EPL = LpT<DT>::EPL, ES = LpT<DT>::ES, U = kLpSlots;
@@ -700,6 +709,9 @@ inline int64_t cd(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+// Enough workgroups to fill the chip four times over, of 4096 logits or more.  One row of
+// 128256 with 20 alternatives: 13.8 us, as with splits of 2048 and 8192; of 16384 16.8.  More
+// than 1024 workgroups were no faster for any number of rows, and rows of one piece need no join.
 int lp_splits(int64_t N, int64_t V, int) {
   const int64_t want = N > 0 ? 1024 / N : 1, most = cd(V, 4096);
   int64_t s = want < most ? want : most;
