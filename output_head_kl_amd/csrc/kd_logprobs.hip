@@ -7,10 +7,10 @@
 // rises; lanes, waves and vocabulary splits are joined by the same rule in double.
 //
 // Bound by reading the logits once: 4096 rows of 128256 bf16 logits (1.05 GB) take 181 us, 5.8
-// TB/s, and 204 us with 8 alternatives; 1037 rows of 32003 float32 logits, a third of them
+// TB/s, and 197 us with 8 alternatives; 1037 rows of 32003 float32 logits, a third of them
 // masked, 26 us (5.1 TB/s).  Few rows are bound by latency: one row of 128256 takes 5.3 us in
-// two launches (the splits and their join), 13.8 us with 20 alternatives, whose selection is a
-// chain of sorting steps in each.
+// two launches (the splits and their join), 13.1 us with 20 alternatives, whose selection is a
+// chain of short dependent steps in each.
 #include "kd_ops.h"
 
 #include <cstdint>
@@ -28,6 +28,7 @@ template <> struct LpT<1> { static constexpr int EPL = 8, ES = 2; };
 template <> struct LpT<0> { static constexpr int EPL = 4, ES = 4; };
 
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+#define LDS_AS __attribute__((address_space(3)))
 
 // 16 bytes at any alignment of the element type (rows of an odd length or stride).
 __device__ __forceinline__ u4 load16(const char *p) {
@@ -153,7 +154,7 @@ __device__ __forceinline__ uint64_t wave_merge(uint64_t a, uint64_t b, int lane)
   return sort_down<32>(a > r ? a : r, lane, true);  // the larger ones are bitonic
 }
 // Of n keys in LDS, any order, the 64 largest, descending.
-__device__ __forceinline__ uint64_t wave_best(const volatile uint64_t *keys, int n, int lane) {
+__device__ __forceinline__ uint64_t wave_best(const LDS_AS uint64_t *keys, int n, int lane) {
   uint64_t list = 0;
   for (int i = 0; i < n; i += 64) {
     const uint64_t v = wave_sort(i + lane < n ? keys[i + lane] : (uint64_t)0, lane);
@@ -181,10 +182,12 @@ struct WaveTop {
   float thr;
   unsigned tie;
   int cnt, notes, masked, top, lane;
-  volatile uint64_t *buf;
-  volatile unsigned *note;
-  __device__ __forceinline__ void init(int top_, int epl, int lane_, volatile uint64_t *b,
-                                       volatile unsigned *n) {
+  // the wave's own: fences stand between its lanes' writes and reads (volatile accesses would
+  // each be waited for)
+  LDS_AS uint64_t *buf;
+  LDS_AS unsigned *note;
+  __device__ __forceinline__ void init(int top_, int epl, int lane_, LDS_AS uint64_t *b,
+                                       LDS_AS unsigned *n) {
     thr = -INFINITY;
     masked = (top_ + epl - 1) / epl;
     tie = ~0u;
@@ -256,6 +259,24 @@ struct WaveTop {
         r = load16(at(from));
         i += 64;
         j = 0;
+        float x[EPL];
+        unpack<DT>(r, x);
+        uint64_t in[EPL];
+        int all = cnt;
+#pragma unroll
+        for (int q = 0; q < EPL; ++q) {
+          in[q] = __builtin_amdgcn_ballot_w64(has && from + q >= e && above(x[q], from + q));
+          all += __popcll(in[q]);
+        }
+        if (all <= kLpBuf) {  // nearly always: no cut between them
+#pragma unroll
+          for (int q = 0; q < EPL; ++q) {
+            if (in[q] >> lane & 1) buf[cnt + prefix(in[q])] = sel_key(x[q], from + q);
+            cnt += __popcll(in[q]);
+          }
+          j = EPL - 1;
+          continue;
+        }
       }
       // room for 64 more (the cut is long, and so in one place)
       if (cnt > (done ? most : kLpBuf - 64)) cut();
@@ -380,9 +401,9 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
   float run[U];   // the largest element so far at each lane and slot
 #pragma unroll
   for (int u = 0; u < U; ++u) run[u] = -INFINITY;
-  volatile float *thr_of = s_thr;
   if (TOP) {
-    wt.init(a.top, EPL, lane, s_buf + w * kLpBuf, s_note + w * kLpNotes);
+    wt.init(a.top, EPL, lane, (LDS_AS uint64_t *)s_buf + w * kLpBuf,
+            (LDS_AS unsigned *)s_note + w * kLpNotes);
     if (t < NW) s_thr[t] = -INFINITY;
     if (t == 0) s_n = 0;
     __syncthreads();
@@ -459,11 +480,13 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
       } else {
         wt.raise(wave_nth(run, a.top));
       }
-      if (lane == 0) thr_of[w] = wt.thr;
+      if (lane == 0)
+        __hip_atomic_store(&s_thr[w], wt.thr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
       fresh = 0;
     }
 #pragma unroll
-    for (int i = 0; i < NW; ++i) wt.raise(thr_of[i]);
+    for (int i = 0; i < NW; ++i)
+      wt.raise(__hip_atomic_load(&s_thr[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
     const int before = wt.notes;
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -502,7 +525,8 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
     s_m[w] = m;
     s_S[w] = S;
     s_T[w] = T;
-    if (TOP) s_thr[w] = wt.thr;
+    if (TOP)
+      __hip_atomic_store(&s_thr[w], wt.thr, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
   }
   __syncthreads();
   const long long at = (long long)row * a.S + split;
@@ -538,7 +562,7 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
     if (n <= 64) {
       place_top<64>(s_pool, n, a.top, lane, write);
     } else {
-      const uint64_t list = wave_best(s_pool, n, lane);
+      const uint64_t list = wave_best((const LDS_AS uint64_t *)s_pool, n, lane);
       if (lane < a.top) write(lane, list);
     }
   }
@@ -710,7 +734,8 @@ inline int64_t cd(int64_t a, int64_t b) { return (a + b - 1) / b; }
 }  // namespace
 
 // Enough workgroups to fill the chip four times over, of 4096 logits or more.  One row of
-// 128256 with 20 alternatives: 13.8 us, as with splits of 2048 and 8192; of 16384 16.8.  More
+// 128256 with 20 alternatives: 13.8 us when this was chosen, as with splits of 2048 and 8192;
+// of 16384 16.8.  More
 // than 1024 workgroups were no faster for any number of rows, and rows of one piece need no join.
 int lp_splits(int64_t N, int64_t V, int) {
   const int64_t want = N > 0 ? 1024 / N : 1, most = cd(V, 4096);
