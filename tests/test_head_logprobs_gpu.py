@@ -108,6 +108,15 @@ def test_tiles_of_both_heights(torch_cuda, N, d, V, chunk):
     test_gradients(torch_cuda, "bf16", N, d, V, chunk, "all")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,d,V", [(300, 8, 1), (300, 64, 2), (70, 8, 5), (65, 72, 40), (1, 8, 1),
+                                   (64, 16, 17)])
+def test_vocabularies_smaller_than_a_tile(torch_cuda, dtype, N, d, V):
+    test_forward(torch_cuda, dtype, N, d, V, 4096)
+    if V > 2:
+        test_gradients(torch_cuda, dtype, N, d, V, 4096, "all")
+
+
 @pytest.mark.parametrize("dw", ["bf16", "f32"])
 @pytest.mark.parametrize("N,d,V", [(1, 8, 3), (1, 1000, 513), (5, 136, 2050), (16, 520, 700),
                                    (17, 264, 3001), (33, 1032, 1111), (48, 64, 20000),
