@@ -733,15 +733,30 @@ inline int64_t cd(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Enough workgroups to fill the chip four times over, of 4096 logits or more.  One row of
-// 128256 with 20 alternatives: 13.8 us when this was chosen, as with splits of 2048 and 8192;
-// of 16384 16.8.  More
-// than 1024 workgroups were no faster for any number of rows, and rows of one piece need no join.
-int lp_splits(int64_t N, int64_t V, int) {
-  const int64_t want = N > 0 ? 1024 / N : 1, most = cd(V, 4096);
-  int64_t s = want < most ? want : most;
-  if (s > kLpMaxSplits) s = kLpMaxSplits;
-  return s < 1 ? 1 : (int)s;
+// Splits of a row, the number with the least estimated time (ns): the rounds of one workgroup
+// per compute unit that a piece each makes, at 20 bytes a ns and unit, half as much again where
+// there is only one workgroup to a unit; the join; and what each workgroup costs by itself.  (Not
+// a function of the alternatives, so that their number changes no other result.)  Against 1024
+// workgroups or as many as pieces of 4096 allow: 400 rows of 32000 bf16 logits, none: 11.3 -> 8.5
+// us, 8: 19.7 -> 15.3 (unsplit); 48 rows of 201088, 5: 17.7 -> 16.4 (ten pieces, not 21); 200
+// rows of 128256, 20: 28 either way (five; unsplit 32).
+int lp_splits(int64_t N, int64_t V, int dtype) {
+  const int64_t most = cd(V, 4096) < kLpMaxSplits ? cd(V, 4096) : kLpMaxSplits;
+  if (N < 1 || N > 512) return 1;  // 600 rows of 128256: 31 us whole, 32.8 in halves
+  const double row = (double)(V * (dtype == 1 ? 2 : 4)) / 20.0;
+  double best = 0.0;
+  int s = 1;
+  for (int64_t c = 1; c <= most; ++c) {
+    const int64_t rounds = (N * c + 255) / 256;
+    const double lone = rounds == 1 ? 1.5 : 1.0;
+    const double t = lone * (double)rounds / (double)c * row + (c > 1 ? 5000.0 : 0.0) +
+                     2.0 * (double)(N * c);
+    if (c == 1 || t < best) {
+      best = t;
+      s = (int)c;
+    }
+  }
+  return s;
 }
 
 size_t lp_workspace(int64_t N, int64_t V, int32_t top, int dtype) {

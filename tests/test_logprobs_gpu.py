@@ -70,6 +70,30 @@ def test_equal_logits_go_to_the_lowest_index(torch_cuda, dtype, N, V, levels):
     _check(torch, logits, tokens, 64)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,pad", [(8, 150001, 1), (24, 100003, 0), (9, 262144, 3), (120, 130008, 0)])
+@pytest.mark.parametrize("top", [1, 20, 64])
+def test_long_rows_in_pieces(torch_cuda, dtype, N, V, pad, top):
+    """Rows long enough to be split over workgroups: pieces without a finite logit, candidates
+    in one piece only, equal ones in all, NaN in one piece, the given token anywhere."""
+    torch = torch_cuda
+    logits, tokens = make_rows(torch, N, V, _dt(torch, dtype), N + V, masked=True, pad=pad)
+    logits[0] = float("-inf")
+    logits[1, : V - 70] = float("-inf")       # all of it in the last piece
+    logits[2, 70:] = float("-inf")            # in the first
+    logits[3] = 1.5                           # equal everywhere
+    logits[4] = torch.finfo(logits.dtype).min
+    logits[5, V // 2] = float("nan")
+    logits[6, V - 1] = float("inf")
+    logits[7, : V // 2] = float("-inf")
+    tokens[1], tokens[2], tokens[3], tokens[4] = V - 1, 0, V // 3, -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = kd.token_logprobs(logits, tokens, top=top, status=status)
+    z = np64(logits)
+    check_forward(outs, z, ref.forward(z, tokens.cpu().numpy(), top), top)
+    assert status.item() == 2
+
+
 def test_rows_that_rise_and_fall(torch_cuda):
     """Every step raises the running maximum, or none does after the first."""
     torch = torch_cuda
