@@ -8,8 +8,7 @@
 // eighth of k ahead.  4096 tokens, d 1024, V 32000 run at 123 TFLOP/s forward and 120 over the
 // three products of the gradients (a library's plain product of that shape at 140, the 256 x
 // 256 tile of kd_gemm.h at 121), but small shapes fill the chip: 512 tokens, d 256, V 8192 take
-// 29 us forward instead of 84.  Below two workgroups of 128 x 128 per compute unit the 64 x 64
-// tile is taken.
+// 29 us forward instead of 84.
 #pragma once
 
 #include "kd_gemm.h"
@@ -24,8 +23,13 @@ template <int T> constexpr int mc_pitch() { return T * 4 + 16; }
 template <int T, int KIND> constexpr int bytes() {
   return KIND == OP_KC ? T * BK * 4 : BK * mc_pitch<T>();
 }
+// The tile with less work on the fullest compute unit, in 64 x 64 tiles: those run 8 % slower
+// per element (2048 tokens, d 512, V 8192 forward: 161 against 149 us) but fill the chip more
+// evenly (1203 tokens, d 2680, V 8047: 493 against 546 us), and a lone large one waits more.
 inline int tile(int64_t m, int64_t n, int64_t splits) {
-  return ((m + 127) / 128) * ((n + 127) / 128) * splits < 512 ? 64 : 128;
+  auto fullest = [&](int64_t t) { return ((m + t - 1) / t * ((n + t - 1) / t) * splits + 255) / 256; };
+  const double large = 4.0 * (double)fullest(128) * (fullest(128) == 1 ? 1.1 : 1.0);
+  return 1.08 * (double)fullest(64) < large ? 64 : 128;
 }
 
 // Chunk q = t + 256 i of a stage: (mn, k) and its place in LDS.

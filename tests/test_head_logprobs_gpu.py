@@ -108,6 +108,15 @@ def test_tiles_of_both_heights(torch_cuda, N, d, V, chunk):
     test_gradients(torch_cuda, "bf16", N, d, V, chunk, "all")
 
 
+@pytest.mark.parametrize("N,d,V,chunk", [
+    (1000, 1000, 16380, 4096),  # tiles of 128 x 128 in all four products
+    (300, 72, 70001, 150),  # of 64 x 64, in two chunks
+    (1000, 264, 16380, 512)])  # of both, the last chunk shorter
+def test_float32_tiles_of_both_sizes(torch_cuda, N, d, V, chunk):
+    test_forward(torch_cuda, "f32", N, d, V, chunk)
+    test_gradients(torch_cuda, "f32", N, d, V, chunk, "all")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,d,V", [(300, 8, 1), (300, 64, 2), (70, 8, 5), (65, 72, 40), (1, 8, 1),
                                    (64, 16, 17)])
