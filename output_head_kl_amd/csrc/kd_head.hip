@@ -175,22 +175,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_head_join(const float2 *part,
   lp_finish(out, r, m, S, T, lp_log(m, S), tok, V, tok >= 0 && tok < V ? zt[r] : 0.f);
 }
 
-// Per token of a chunk, what the gradient's epilogue reads: l2 = lse log2 e, and dz =
-// p (a + b log2 p) + g [v = tok].
-__global__ void k_head_coef(Tokens tokens, LpGrad g, int rows, int V, float *l2, float *a,
-                            float *b, float *gt, int *tok32) {
+__global__ void k_head_coef(Tokens tokens, LpGrad g, int rows, int V, HeadCoef k) {
   const int r = blockIdx.x * blockDim.x + threadIdx.x;
   if (r >= rows) return;
-  const long long tok = tokens.at(r);
-  float gl = g.g_logp && tok >= 0 ? g.g_logp[r] : 0.f;
-  if (tok >= V) gl = __uint_as_float(0x7FC00000u);
-  const float ge = g.g_entropy ? g.g_entropy[r] : 0.f, gz = g.g_lse ? g.g_lse[r] : 0.f;
-  const float2 st = g.stats[r];
-  l2[r] = (float)(((double)st.x + (double)st.y) * 1.4426950408889634);
-  a[r] = (gz - gl) - ge * g.entropy[r];
-  b[r] = (float)(-(double)ge * kOpLn2d);
-  gt[r] = gl;
-  tok32[r] = tok >= 0 && tok < V ? (int)tok : -1;
+  const HeadTok c = head_tok(tokens, g, r, V);
+  k.l2[r] = c.l2;
+  k.a[r] = c.a;
+  k.b[r] = c.b;
+  k.g[r] = c.g;
+  k.tok[r] = c.tok;
 }
 
 template <int DT>
@@ -483,7 +476,7 @@ hipError_t launch_head_join(bool few, const float2 *part, const float *part_t, i
 hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows, int64_t V,
                             const HeadCoef &k, hipStream_t s) {
   hipLaunchKernelGGL(k_head_coef, dim3(cdiv(rows, 256)), dim3(256), 0, s, tokens, g, (int)rows,
-                     (int)V, k.l2, k.a, k.b, k.g, k.tok);
+                     (int)V, k);
   return hipGetLastError();
 }
 

@@ -230,7 +230,8 @@ struct FewBwd {
   const char *W, *h;
   const unsigned short *ht;  // (j, c) at j * 256 + c, zero for c >= rows
   int rows, d, V;
-  HeadCoef k;
+  Tokens tokens;
+  LpGrad g;
   unsigned short *dz;        // null, or per 32 vocabulary rows [hi, lo][16 tokens][8 rows][16][8]
   void *dW;                  // null, or [V][d] of type OUT
   int stream;                // dW is larger than the last-level cache
@@ -253,15 +254,13 @@ __global__ __launch_bounds__(kFewThreads) void k_head_few_bwd(FewBwd a) {
   for (int n = 0; n < NC; ++n) {
     const int c = n * 16 + (lane & 15);
     const bool cv = c < a.rows;
-    const float l2 = cv ? a.k.l2[c] : 0.f, ca = cv ? a.k.a[c] : 0.f, cb = cv ? a.k.b[c] : 0.f;
-    const float cg = cv ? a.k.g[c] : 0.f;
-    const int ct = cv ? a.k.tok[c] : -1;
+    const HeadTok k = cv ? head_tok(a.tokens, a.g, c, a.V) : HeadTok{0.f, 0.f, 0.f, 0.f, -1};
     unsigned short hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int v = v0 + g * 4 + i;
-      const float q = fmaf(acc[0][n][i], kLog2e, -l2);  // log2 p
-      float x = fmaf(fast_exp2(q), fmaf(cb, q, ca), v == ct ? cg : 0.f);
+      const float q = fmaf(acc[0][n][i], kLog2e, -k.l2);  // log2 p
+      float x = fmaf(fast_exp2(q), fmaf(k.b, q, k.a), v == k.tok ? k.g : 0.f);
       if (!cv || v >= a.V) x = 0.f;
       hi[i] = f32_to_bf16(x);
       lo[i] = f32_to_bf16(x - bf16_to_f32(hi[i]));
@@ -547,10 +546,10 @@ int head_few_dh_splits(int64_t d, int64_t V) {
 }
 
 hipError_t launch_head_few_bwd(const void *W, const void *h, const void *ht, int64_t rows,
-                               int64_t d, int64_t V, int64_t V_pad, const HeadCoef &k, void *dz,
-                               void *dW, int out, hipStream_t s) {
+                               int64_t d, int64_t V, int64_t V_pad, const Tokens &tokens,
+                               const LpGrad &g, void *dz, void *dW, int out, hipStream_t s) {
   const FewBwd a{(const char *)W, (const char *)h, (const unsigned short *)ht, (int)rows, (int)d,
-                 (int)V, k, (unsigned short *)dz, dW,
+                 (int)V, tokens, g, (unsigned short *)dz, dW,
                  V * d * (out == 1 ? 2 : 4) > ((int64_t)256 << 20)};
   if (out == 1) run_head_few_bwd<1>(a, V_pad, s);
   else run_head_few_bwd<0>(a, V_pad, s);

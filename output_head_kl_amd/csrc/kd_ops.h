@@ -101,6 +101,22 @@ hipError_t launch_head_few(int dtype, const void *W, const void *h, int64_t rows
 hipError_t launch_head_join(bool few, const float2 *part, const float *part_t, int64_t n_lse,
                             int64_t ld_part, int64_t rows, int64_t V, const float *zt,
                             const Tokens &tokens, const LpOut &out, hipStream_t s);
+// Per token, what the gradient's epilogue reads: l2 = lse log2 e, and dz = p (a + b log2 p) +
+// g [v = tok], tok -1 where there is none in range.
+struct HeadTok {
+  float l2, a, b, g;
+  int tok;
+};
+__device__ __forceinline__ HeadTok head_tok(const Tokens &tokens, const LpGrad &g, int r, int V) {
+  const long long tok = tokens.at(r);
+  float gl = g.g_logp && tok >= 0 ? g.g_logp[r] : 0.f;
+  if (tok >= V) gl = __uint_as_float(0x7FC00000u);
+  const float ge = g.g_entropy ? g.g_entropy[r] : 0.f, gz = g.g_lse ? g.g_lse[r] : 0.f;
+  const float2 st = g.stats[r];
+  return {(float)(((double)st.x + (double)st.y) * 1.4426950408889634),
+          (gz - gl) - ge * g.entropy[r], (float)(-(double)ge * kOpLn2d), gl,
+          tok >= 0 && tok < V ? (int)tok : -1};
+}
 struct HeadCoef {  // per token of a chunk
   float *l2, *a, *b, *g;
   int *tok;
@@ -113,8 +129,8 @@ hipError_t launch_head_coef(const Tokens &tokens, const LpGrad &g, int64_t rows,
 inline int head_few_tokens(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 int head_few_dh_splits(int64_t d, int64_t V);
 hipError_t launch_head_few_bwd(const void *W, const void *h, const void *ht, int64_t rows,
-                               int64_t d, int64_t V, int64_t V_pad, const HeadCoef &k, void *dz,
-                               void *dW, int out, hipStream_t s);
+                               int64_t d, int64_t V, int64_t V_pad, const Tokens &tokens,
+                               const LpGrad &g, void *dz, void *dW, int out, hipStream_t s);
 hipError_t launch_head_few_dh(const void *W, const void *dz, int64_t rows, int64_t d, int64_t V,
                               int64_t V_pad, int nsplit, float *part, void *dh, hipStream_t s);
 // dz as blocks of 256 vocabulary columns (element (c, v) at (v / 256) * C_alloc * 256 + c * 256

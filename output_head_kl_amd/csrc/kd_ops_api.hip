@@ -128,7 +128,7 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, int dtyp
     off += (size_t)rup(bytes, 256);
     return o;
   };
-  L.off_coef = take(5 * L.C_alloc * 4);
+  L.off_coef = take(L.few ? 0 : 5 * L.C_alloc * 4);
   L.off_dz = take(!L.few ? L.C_alloc * L.V_pad * es : want_dh ? 2 * tok * L.V_pad * 2 : 0);
   L.off_dhpart =
       take(!want_dh ? 0 : L.nsplit * 4 * (L.few ? tok * rup(d, 128) : L.C_alloc * L.d_pad));
@@ -394,12 +394,10 @@ int kd_head_logprobs_bwd(const void *h, const void *W, int32_t dtype, const void
   if (L.few) {
     const kd::LpGrad g{(const float2 *)row_stats, entropy, grad_logp, grad_entropy, grad_lse};
     void *ht = ws + L.off_ht;
-    LAUNCH(kd::KC_LOGPROBS_BWD,
-           kd::launch_head_coef(tokens_at(tokens, token_bits, 0), g, N, V, k, stream));
     if (dW) LAUNCH(kd::KC_TRANSPOSE, kd::launch_transpose_h(h, N, d, L.C_alloc, ht, tst_h, stream));
     LAUNCH(kd::KC_BWD_GEMM,
-           kd::launch_head_few_bwd(W, h, ht, N, d, V, L.V_pad, k, dh ? dz : nullptr, dW, dw_dtype,
-                                   stream));
+           kd::launch_head_few_bwd(W, h, ht, N, d, V, L.V_pad, tokens_at(tokens, token_bits, 0), g,
+                                   dh ? dz : nullptr, dW, dw_dtype, stream));
     if (dh)
       LAUNCH(kd::KC_DH_GEMM, kd::launch_head_few_dh(W, dz, N, d, V, L.V_pad, L.nsplit, dhpart, dh,
                                                     stream));
