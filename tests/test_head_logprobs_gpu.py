@@ -164,6 +164,39 @@ def test_few_tokens_gradients_are_rounded_once(torch_cuda, N, d, V, dw):
         assert off.max() <= 0, f"{name}: {off.max():.3g} past the tolerance"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 70])
+def test_heads_past_32_bit_offsets(torch_cuda, dtype, N):
+    """W and dW of 2.17e9 elements; the reference is float64 on the GPU, in parts of W."""
+    torch = torch_cuda
+    d, V, part = 4096, 530000, 53000
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(8)
+    h = torch.randn((N, d), generator=g, device="cuda").to(dt)
+    W = torch.empty((V, d), dtype=dt, device="cuda")
+    for v in range(0, V, part):
+        W[v:v + part] = torch.randn((part, d), generator=g, device="cuda") * (2 / d ** 0.5)
+    tokens = torch.randint(0, V, (N,), generator=g, device="cuda")
+    tokens[0], tokens[1], tokens[2] = V - 1, -1, V - 4000
+    up = torch.randn(N, generator=g, device="cuda")
+    hx, wx = h.detach().requires_grad_(), W.detach().requires_grad_()
+    outs = kd.head_logprobs(hx, wx, tokens)
+    dh, dW = torch.autograd.grad(outs[0], (hx, wx), up)
+    z = torch.cat([h.double() @ W[v:v + part].double().t() for v in range(0, V, part)], 1)
+    lse = z.logsumexp(1)
+    ez = 6 * (d + 1) ** 0.5 * U * float((h.double().norm(dim=1)[:, None] * 2.3).max())
+    given = tokens >= 0
+    logp = torch.where(given, z.gather(1, tokens.clamp(min=0)[:, None])[:, 0] - lse, 0.0)
+    assert (outs[2].double() - lse).abs().max().item() <= ez + 1e-5
+    assert (outs[0].double() - logp).abs().max().item() <= 2 * ez + 2e-5
+    dz = -(z - lse[:, None]).exp() * (up.double() * given)[:, None]
+    dz[given.nonzero()[:, 0], tokens[given]] += up.double()[given]
+    want = sum(dz[:, v:v + part] @ W[v:v + part].double() for v in range(0, V, part))
+    check_grad("dh", dh, np64(want), dtype)
+    for rows in (slice(V - 4096, V), slice(260000, 264000), slice(0, 500)):
+        check_grad("dW", dW[rows], np64(dz[:, rows].t() @ h.double()), dtype)
+
+
 def test_infinite_logits_make_the_row_invalid(torch_cuda):
     """An infinite weight: -inf or +inf logits, so NaN in the row's results, status set."""
     torch = torch_cuda
