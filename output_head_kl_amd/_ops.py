@@ -9,6 +9,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -411,6 +412,11 @@ _head_backward_once = torch.autograd.function.once_differentiable(_head_backward
 
 
 # ---- gradient norm and clipping -------------------------------------------------------------
+# what is asked of each of many tensors: unbound, as map calls these faster than a loop would
+_device_of, _contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_numel, _address, _dtype_of = torch.Tensor.numel, torch.Tensor.data_ptr, operator.attrgetter("dtype")
+
+
 def _clip(grads, max_norm, out, workspace, stream):
     if not grads:
         raise ValueError("no tensors")
@@ -422,24 +428,23 @@ def _clip(grads, max_norm, out, workspace, stream):
     n = len(grads)
     if out is not None and len(out) != n:
         raise ValueError(f"{len(out)} outputs for {n} gradients")
-    on = dev.index
     for name, ts in (("grads", grads), ("out", out or ())):
-        for i, t in enumerate(ts):
-            if t.get_device() != on:
+        if (list(map(_device_of, ts)).count(dev.index) != len(ts)
+                or list(map(_contiguous, ts)).count(True) != len(ts)):
+            for i, t in enumerate(ts):
                 kd._on_device(dev, **{f"{name}[{i}]": t})
-            if not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be contiguous")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}[{i}] must be contiguous")
     try:
-        types = [_CODES[t.dtype] for t in grads]
+        types = [_CODES[d] for d in map(_dtype_of, grads)]
     except KeyError as e:
         raise TypeError(f"gradients must be bfloat16 or float32, not {e.args[0]}") from None
-    sizes = [t.numel() for t in grads]
-    if out is not None and (sizes != [t.numel() for t in out]
-                            or types != [_CODES.get(t.dtype) for t in out]):
+    sizes = list(map(_numel, grads))
+    if out is not None and (sizes != list(map(_numel, out))
+                            or types != list(map(_CODES.get, map(_dtype_of, out)))):
         raise ValueError("out must have the shapes and dtypes of grads")
     held = [array.array("q", sizes), array.array("i", types),
-            array.array("Q", [t.data_ptr() for t in grads]),
-            array.array("Q", [t.data_ptr() for t in out or ()])]
+            array.array("Q", map(_address, grads)), array.array("Q", map(_address, out or ()))]
     numel, types, gp, op = (a.buffer_info()[0] for a in held)
     op = op if out is not None else None
     if workspace is None:
