@@ -498,11 +498,6 @@ hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t row
   return g32::run<OP_KC, OP_KC>(g32::tile(V_pad, rows, 1), V_pad, rows, 1, d, d, A, B, e, s);
 }
 
-// The copy costs a read and a write of W, and lets the product read both operands without
-// transposing them in LDS, on a 384-row tile.  201088 x 2880: with the copy 1.49 against 1.07 ms
-// for all gradients of 48 tokens, 12.48 against 13.42 ms for those of 4096.
-bool head_wt(int64_t N) { return N > 1024; }
-
 // The float32 tile of the dh product, which has up to 32 splits to fill the chip.
 static int dh_tile32(int64_t C_alloc, int64_t d) { return g32::tile(d, C_alloc, 32); }
 
@@ -526,6 +521,29 @@ void head_dh_splits(int dtype, bool wt, int64_t C_alloc, int64_t d, int64_t V_pa
   }
   *k_split = ((V_pad + ns - 1) / ns + kTile - 1) / kTile * kTile;
   *nsplit = (int)((V_pad + *k_split - 1) / *k_split);
+}
+
+// The copy costs a read and a write of W, and lets the dh product read both operands without
+// transposing them in LDS, on a 384-row tile.  Up to 1024 tokens it does not pay (512, d 4096, V
+// 128256: all gradients 2.10 ms with it, 1.76 without), above 4096 it does (16384, 2048, 128256:
+// 21.8 and 23.7 ms).  Between, the two are compared in units of the product without it on a full
+// chip, 18 % longer there: what the rounds leave empty (which measured more than its share,
+// hence the power), rows past d, and the copy, 580 / N.  2048 tokens, d 1024, V 32000: 529 and
+// 431 us; 4096, 2880, 201088: 12.1 and 13.4 ms.
+bool head_wt(int64_t N, int64_t C_alloc, int64_t d, int64_t V_pad) {
+  if (N <= 1024 || N > 4096) return N > 4096;
+  auto cost = [&](bool wt) {
+    int ns;
+    int64_t ks;
+    head_dh_splits(1, wt, C_alloc, d, V_pad, &ns, &ks);
+    const int64_t tm = wt ? dh_tile16(d) : kTile, rows = (d + tm - 1) / tm * tm;
+    const int64_t tiles = rows / tm * (C_alloc / kTile), rounds = (tiles * ns + 255) / 256;
+    const double e = (double)(V_pad * tiles) / (double)(rounds * 256 * ks);
+    const double t = (double)rows / (double)d / (e * e * e * e);
+    if (!wt) return rounds == 1 ? t : 1.12 * t;
+    return t / (tm == kTile ? 1.18 / kRowGain : 1.18) + 580.0 / (double)N;
+  };
+  return cost(true) < cost(false);
 }
 
 // D[j][c] = sum_v W[v][j] dz[c][v]

@@ -139,9 +139,10 @@ hipError_t launch_head_dz(int dtype, const void *W, const void *h_c, int64_t row
                           int64_t V, const HeadCoef &k, void *dz, void *dzt, int64_t tst,
                           int64_t V_pad, int64_t C_alloc, hipStream_t s);
 
-// Whether the dh product of a call with N tokens reads a k-contiguous copy of W (bf16), and
-// into how many vocabulary splits (of k_split entries, a multiple of 256) it goes.
-bool head_wt(int64_t N);
+// Whether the dh product of a call with N tokens in chunks of C_alloc reads a k-contiguous copy
+// of W (bf16), and into how many vocabulary splits (of k_split entries, a multiple of 256) it
+// goes.
+bool head_wt(int64_t N, int64_t C_alloc, int64_t d, int64_t V_pad);
 void head_dh_splits(int dtype, bool wt, int64_t C_alloc, int64_t d, int64_t V_pad, int *nsplit,
                     int64_t *k_split);
 // dh partials [nsplit][C_alloc][d_pad]; bf16 reads W through WT (launch_transpose_w), or itself

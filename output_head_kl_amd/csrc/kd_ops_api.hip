@@ -118,7 +118,7 @@ HeadBwd head_bwd_layout(int64_t N, int64_t d, int64_t V, int64_t chunk, int dtyp
   L.d_pad = rup(d, kd::kTile);
   L.nchunks = (n + L.C - 1) / L.C;
   L.group = !bf16 || group < 1 ? 1 : group < L.nchunks ? group : L.nchunks;
-  L.wt = bf16 && kd::head_wt(N);
+  L.wt = bf16 && !L.few && kd::head_wt(n, L.C_alloc, d, L.V_pad);
   if (L.few) L.nsplit = kd::head_few_dh_splits(d, V);
   else kd::head_dh_splits(dtype, L.wt, L.C_alloc, d, L.V_pad, &L.nsplit, &L.k_split);
   const int64_t tok = kd::head_few_tokens(n);

@@ -99,9 +99,11 @@ def test_gradients(torch_cuda, dtype, N, d, V, chunk, which):
 @pytest.mark.parametrize("N,d,V,chunk", [
     (300, 72, 70001, 2048),  # vocabulary tiles of 384 rows, a ragged last one
     (700, 264, 40000, 300),  # the same in three chunks, the last of 100 rows
-    (1100, 264, 2050, 1100),  # dh from a copy of W: one tile of 384 hidden units
-    (1100, 512, 2050, 600),  # two of 256, two chunks of different length
-    (1030, 1000, 1999, 515)])
+    (1100, 264, 2050, 1100),  # dh from W or a copy of it, 264 hidden units
+    (1100, 512, 2050, 600),  # two chunks of different length
+    (1030, 1000, 1999, 515),
+    (4200, 264, 1111, 2100),  # above 4096 tokens dh always reads a copy of W
+    (4200, 512, 777, 1500)])
 def test_tiles_of_both_heights(torch_cuda, N, d, V, chunk):
     """bf16 above 64 tokens: the products choose 256 or 384 rows of W (or of its copy) a tile."""
     test_forward(torch_cuda, "bf16", N, d, V, chunk)
