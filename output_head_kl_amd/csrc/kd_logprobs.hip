@@ -493,7 +493,8 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(LpArgs a) {
       wt.look(lu[u], (unsigned)e0 + ((step * U + u) * NT + t) * EPL);
     fresh += wt.notes - before;
     if (wt.notes > kLpNotes - 64 * U || end)
-      wt.template drain<DT>((unsigned)e0 + len, a.S > 1 ? kLpBuf : 64, [&](unsigned i) { return rp + (size_t)i * ES; });
+      wt.template drain<DT>((unsigned)e0 + len, a.S > 1 ? kLpBuf : 64,
+                            [&](unsigned i) { return rp + (size_t)i * ES; });
   };
 
   if (len >= EPL) {
@@ -771,7 +772,8 @@ void run_token_logprobs(const LpArgs &a, hipStream_t s) {
   if (a.V <= 2048)
     hipLaunchKernelGGL((k_token_logprobs<DT, TOP, 64, 2>), grid, dim3(64), 0, s, a);
   else
-    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, kLpThreads, kLpSlots>), grid, dim3(kLpThreads), 0, s, a);
+    hipLaunchKernelGGL((k_token_logprobs<DT, TOP, kLpThreads, kLpSlots>), grid, dim3(kLpThreads),
+                       0, s, a);
   if (a.S > 1)
     hipLaunchKernelGGL((k_token_logprobs_join<DT, TOP>), rows, dim3(kLpThreads), 0, s, a);
 }
